@@ -15,6 +15,8 @@ _API = (
     "dn_accept_greedy_noalloc",
     # drafts from the request's own context; prefix-cache index
     "dn_context_drafts", "PrefixCache",
+    # paged cache of the attention layers: write, read back, attend
+    "dn_kv_append", "dn_kv_gather", "dn_attn_paged", "dn_attn_workspace_bytes", "attn_workspace",
     # bounded-wait diagnostics
     "dn_prefill_wait_timeouts", "dn_wait_selftest",
     # errors and loading

@@ -16,14 +16,16 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libdn.so")
 
 DN_OK, DN_ERR_INVALID_ARG, DN_ERR_UNSUPPORTED, DN_ERR_CUDA = 0, 1, 2, 3
-DN_F16, DN_F32 = 0, 1
+DN_F16, DN_F32, DN_BF16, DN_E4M3 = 0, 1, 2, 3
 MAX_BLOCK = 16
 PREFILL_CHUNK = 64
 
 _DT = {torch.float16: DN_F16, torch.float32: DN_F32}
+# types of the paged cache and of the tensors that go with it
+_KV_DT = {torch.float16: DN_F16, torch.float32: DN_F32, torch.bfloat16: DN_BF16, torch.float8_e4m3fn: DN_E4M3}
 
 # Every exported symbol of include/dn.h with its ctypes signature.
-_P, _I, _S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_P, _I, _S, _L = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int64
 SIGNATURES = {
     "dn_verify_block": (_I, [_I, _I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
     "dn_accept_workspace_bytes": (_S, [_I, _I, _I]),
@@ -44,6 +46,10 @@ SIGNATURES = {
     "dn_prefix_cache_insert": (_I, [_P, _P, _I, ctypes.c_int32, _P]),
     "dn_prefix_cache_lookup": (_I, [_P, _P, _I, _P, _P]),
     "dn_prefix_cache_size": (_I, [_P]),
+    "dn_kv_append": (_I, [_I] * 9 + [_P, _P, _L, _L] + [_P] * 8),
+    "dn_kv_gather": (_I, [_I] * 9 + [_P] * 10),
+    "dn_attn_workspace_bytes": (_S, [_I] * 5),
+    "dn_attn_paged": (_I, [_I] * 10 + [_P, _L] + [_P] * 7 + [ctypes.c_float, _I, _P, _P, _P, _S, _P]),
     "dn_context_drafts": (_I, [_I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
 }
 
@@ -304,6 +310,109 @@ def dn_context_drafts(context, lengths, n_max=4, n_min=1, K=8, drafts=None, coun
                                           _stream(stream))
     _check("dn_context_drafts", st)
     return drafts, count, match_len
+
+
+def _kv_pool(start, kv_len, page_table, k_cache, v_cache, k_exp, v_exp):
+    """Checks the paged cache's tensors; returns (B, heads, D, page, max_pages, pages)."""
+    _require(k_cache.dim() == 4 and v_cache.shape == k_cache.shape and v_cache.dtype == k_cache.dtype,
+             "k_cache, v_cache [pages,heads,page,D] of one dtype")
+    pages, heads, page, D = k_cache.shape
+    B, max_pages = page_table.shape
+    _dev(start, kv_len, page_table, k_cache, v_cache, k_exp, v_exp)
+    _require(start.dtype == kv_len.dtype == page_table.dtype == torch.int32, "start, kv_len, page_table int32")
+    _require(start.shape == (B + 1,) and kv_len.shape == (B,), "start [B+1], kv_len [B], page_table [B,max_pages]")
+    _require(k_cache.dtype in _KV_DT, "k_cache, v_cache fp16, bf16 or float8_e4m3fn")
+    if k_cache.dtype == torch.float8_e4m3fn:
+        _require(k_exp is not None and v_exp is not None and k_exp.dtype == v_exp.dtype == torch.uint8
+                 and k_exp.shape == v_exp.shape == (pages, heads, page), "an e4m3 cache has k_exp, v_exp [pages,heads,page] uint8")
+    else:
+        _require(k_exp is None and v_exp is None, "k_exp, v_exp go with an e4m3 cache")
+    return B, heads, D, page, max_pages, pages
+
+
+def _rows(t, heads, D, name):
+    """Checks packed rows [total, heads, D], dense inside a row; returns (total, row stride in elements)."""
+    _require(t.is_cuda, "all tensors must be CUDA tensors")
+    _require(t.dim() == 3 and t.shape[1] == heads and t.shape[2] == D, "%s [total,heads,D]" % name)
+    _require(t.stride(2) == 1 and (heads == 1 or t.stride(1) == D), "%s dense inside a row" % name)
+    _require(t.dtype in _KV_DT, "%s fp16 or bf16" % name)
+    return t.shape[0], t.stride(0) if t.shape[0] > 1 else heads * D
+
+
+def dn_kv_append(k, v, start, kv_len, page_table, k_cache, v_cache, k_exp=None, v_exp=None, stream=None):
+    """Write packed rows k, v [total,heads,D] (the newest tokens) to their places in the paged cache.
+
+    start [B+1], kv_len [B] (the newest included), page_table [B,max_pages] int32; k_cache, v_cache
+    [pages,heads,page,D] in k's dtype, or float8_e4m3fn with k_exp, v_exp [pages,heads,page] uint8.
+    k and v may be slices of a wider projection (rows dense inside). Returns (k_cache, v_cache).
+    """
+    B, heads, D, page, max_pages, pages = _kv_pool(start, kv_len, page_table, k_cache, v_cache, k_exp, v_exp)
+    total, ks = _rows(k, heads, D, "k")
+    total_v, vs = _rows(v, heads, D, "v")
+    _require(total_v == total and v.dtype == k.dtype, "v like k")
+    st = load_library().dn_kv_append(
+        B, total, heads, D, page, max_pages, pages, _KV_DT[k.dtype], _KV_DT[k_cache.dtype], _ptr(k), _ptr(v), ks, vs,
+        _ptr(start), _ptr(kv_len), _ptr(page_table), _ptr(k_cache), _ptr(v_cache), _ptr(k_exp), _ptr(v_exp),
+        _stream(stream))
+    _check("dn_kv_append", st)
+    return k_cache, v_cache
+
+
+def dn_kv_gather(start, kv_len, page_table, k_cache, v_cache, k_exp, v_exp, k, v, stream=None):
+    """Read the newest tokens' keys and values back into packed rows k, v [total,heads,D] (dense).
+
+    The cache's tensors as for dn_kv_append (k_exp, v_exp None unless it is e4m3). Returns (k, v).
+    """
+    B, heads, D, page, max_pages, pages = _kv_pool(start, kv_len, page_table, k_cache, v_cache, k_exp, v_exp)
+    _dev(k, v)
+    total, _ = _rows(k, heads, D, "k")
+    _require(v.shape == k.shape and v.dtype == k.dtype, "v like k")
+    st = load_library().dn_kv_gather(
+        B, total, heads, D, page, max_pages, pages, _KV_DT[k.dtype], _KV_DT[k_cache.dtype], _ptr(start), _ptr(kv_len),
+        _ptr(page_table), _ptr(k_cache), _ptr(v_cache), _ptr(k_exp), _ptr(v_exp), _ptr(k), _ptr(v), _stream(stream))
+    _check("dn_kv_gather", st)
+    return k, v
+
+
+def dn_attn_workspace_bytes(B, total, heads_kv, group, D):
+    return int(load_library().dn_attn_workspace_bytes(B, total, heads_kv, group, D))
+
+
+def attn_workspace(q, k_cache, page_table):
+    """A workspace for dn_attn_paged on tensors of these shapes (any contents)."""
+    heads = max(k_cache.shape[1], 1)
+    n = dn_attn_workspace_bytes(page_table.shape[0], q.shape[0], heads, q.shape[1] // heads, q.shape[2])
+    return torch.empty((max(n, 16),), dtype=torch.uint8, device=q.device)
+
+
+def dn_attn_paged(q, start, kv_len, page_table, k_cache, v_cache, k_exp=None, v_exp=None, scale=None, window=0,
+                  out=None, lse=None, workspace=None, stream=None):
+    """Attention of the newest tokens q [total,heads,D] over their requests' cached keys and values.
+
+    The cache's tensors as for dn_kv_append; heads is a multiple of the cache's. scale defaults to
+    D ** -0.5; window is how many tokens a row looks back, itself included (0: all). q may be a slice of
+    a wider projection. Returns (out [total,heads,D] in q's dtype, lse [total,heads] fp32).
+    """
+    B, heads_kv, D, page, max_pages, pages = _kv_pool(start, kv_len, page_table, k_cache, v_cache, k_exp, v_exp)
+    _require(q.dim() == 3 and q.shape[1] % heads_kv == 0 and q.shape[1] > 0, "q's heads a multiple of the cache's")
+    heads = q.shape[1]
+    total, qs = _rows(q, heads, D, "q")
+    if out is None:
+        out = torch.empty((total, heads, D), dtype=q.dtype, device=q.device)
+    if lse is None:
+        lse = torch.empty((total, heads), dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = attn_workspace(q, k_cache, page_table)
+    _dev(out, lse, workspace)
+    _require(out.shape == q.shape and out.dtype == q.dtype, "out [total,heads,D] in q's dtype")
+    _require(lse.shape == (total, heads) and lse.dtype == torch.float32, "lse [total,heads] fp32")
+    st = load_library().dn_attn_paged(
+        B, total, heads_kv, heads // heads_kv, D, page, max_pages, pages, _KV_DT[q.dtype], _KV_DT[k_cache.dtype],
+        _ptr(q), qs, _ptr(start), _ptr(kv_len), _ptr(page_table), _ptr(k_cache), _ptr(v_cache), _ptr(k_exp),
+        _ptr(v_exp), float(D ** -0.5 if scale is None else scale), int(window), _ptr(out), _ptr(lse), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("dn_attn_paged", st)
+    return out, lse
 
 
 class PrefixCache:

@@ -79,7 +79,8 @@ typedef enum {
     DN_ERR_CUDA = 3
 } dn_status;
 
-typedef enum { DN_F16 = 0, DN_F32 = 1 } dn_dtype;
+/* DN_BF16 and DN_E4M3 are types of the paged-cache calls alone (dn_kv_append and after). */
+typedef enum { DN_F16 = 0, DN_F32 = 1, DN_BF16 = 2, DN_E4M3 = 3 } dn_dtype;
 
 /* Largest verify block (7 model drafts + 8 context drafts + 1 [P4]). */
 #define DN_MAX_BLOCK 16
@@ -401,6 +402,95 @@ unsigned int dn_prefill_wait_timeouts(void);
  * two budgets. Errors: DN_ERR_INVALID_ARG (nothing launched), DN_ERR_CUDA (launch failed).
  */
 dn_status dn_wait_selftest(int budget_us, int32_t *result, dn_stream_t stream);
+
+/*
+ * The paged cache of the model's attention layers: dn_kv_append, dn_kv_gather, dn_attn_paged.
+ *
+ * A hybrid model's other layers attend to every earlier token. Their keys and values live in
+ * pages of a pool, kept next to the recurrent state ([P1]); a verify block's tokens are written
+ * behind the request's cached ones, the block attends over the cache, and rejecting drafts is
+ * shortening kv_len ([P3]).
+ *
+ *   k_cache, v_cache  [pages][heads][page][D] cache_dt, 16-byte aligned
+ *   k_exp, v_exp      [pages][heads][page] bytes, 16-byte aligned, for cache_dt = DN_E4M3 only (else
+ *                     NULL): the row of D values is e4m3 * 2^(byte - 127)
+ *   page_table        [B][max_pages] int32: the token at position p of request b is row p % page
+ *                     of pool page page_table[b][p / page]
+ *   kv_len            [B] int32: cached tokens of each request, the newest included; a value below 0
+ *                     counts as 0, one above DN_KV_MAX_TOKENS as that
+ *   start             [B + 1] int32, not decreasing: request b's newest n_b = start[b+1] - start[b]
+ *                     tokens are the packed rows start[b] .. start[b+1]-1 of k, v or q (0 <= start <=
+ *                     total); row start[b] + i is the token at position kv_len[b] - n_b + i. n_b
+ *                     differs between requests and may be 0.
+ *
+ * start, kv_len and page_table are read on the device (no host round trip after an accept). Nothing
+ * in them leads outside the buffers: a position without a page (below 0, beyond max_pages * page, or
+ * with a page id outside 0 .. pages-1) is not written, and reads as zeros.
+ *
+ *   D         64, 128 or 256;  page 16, 32, 64 or 128 (64 is the prefix index's interval)
+ *   io_dt     DN_F16 or DN_BF16;  cache_dt io_dt, or DN_E4M3 for 8 bits
+ *   total     packed rows, 0 .. DN_KV_MAX_ROWS;  max_pages * page <= DN_KV_MAX_TOKENS
+ * Another D, page or type pair gives DN_ERR_UNSUPPORTED. Rows of one request write to pages of its
+ * own; two packed rows that name the same place leave one of them there.
+ *
+ * dn_kv_append -- write the newest tokens' keys and values to their places.
+ *   k, v      row t at k + t * k_stride elements, [heads][D] dense inside; io_dt, 16-byte aligned,
+ *             strides in elements, multiples of 8 and >= heads * D (a slice of a wider projection)
+ * For DN_E4M3 the byte is the least exponent e with max |x| <= 448 * 2^e of the row (plus 127; rows
+ * of zeros get 0), and values are rounded to nearest even. NaN stays NaN and does not count for the
+ * maximum; an infinity becomes the largest value.
+ *
+ * dn_kv_gather -- read the newest tokens' keys and values back.
+ *   k, v      [total][heads][D] io_dt, dense, written; packed rows of no request get zeros. Values
+ *             from 8 bits are rounded to io_dt, and stay finite.
+ */
+#define DN_KV_MAX_ROWS (1 << 28)
+#define DN_KV_MAX_TOKENS (1 << 30)
+dn_status dn_kv_append(int B, int total, int heads, int D, int page, int max_pages, int pages,
+                       dn_dtype io_dt, dn_dtype cache_dt, const void *k, const void *v, int64_t k_stride,
+                       int64_t v_stride, const int32_t *start, const int32_t *kv_len,
+                       const int32_t *page_table, void *k_cache, void *v_cache, uint8_t *k_exp,
+                       uint8_t *v_exp, dn_stream_t stream);
+dn_status dn_kv_gather(int B, int total, int heads, int D, int page, int max_pages, int pages,
+                       dn_dtype io_dt, dn_dtype cache_dt, const int32_t *start, const int32_t *kv_len,
+                       const int32_t *page_table, const void *k_cache, const void *v_cache,
+                       const uint8_t *k_exp, const uint8_t *v_exp, void *k, void *v, dn_stream_t stream);
+
+/*
+ * dn_attn_paged -- attention of each request's newest tokens over its cached ones.
+ *
+ * For every packed row t of request b, at position p = kv_len[b] - n_b + (t - start[b]), and every
+ * query head h = heads of the key head h / group:
+ *   sees j  if  0 <= j <= p, j < kv_len[b], and (window > 0) j > p - window
+ *   x_j = scale * q[t][h] . K_j[h / group];   lse[t][h] = log sum_j exp(x_j)
+ *   out[t][h] = sum_j exp(x_j - lse) V_j[h / group]
+ * The newest tokens' own keys and values are in the cache (append them first), so one call serves a
+ * single new token, a verify block and a chunk of a prompt, also mixed in one batch. A row that
+ * sees nothing gets out = 0 and lse = -inf.
+ *
+ *   heads_kv, group  key heads, and query heads of each (heads_kv * group query heads)
+ *   q         row t at q + t * q_stride elements, [heads_kv * group][D] dense inside; io_dt, 16-byte
+ *             aligned, q_stride a multiple of 8 and >= heads_kv * group * D
+ *   scale     > 0, finite;  window  tokens that a row looks back, itself included; 0: all
+ *   out       [total][heads_kv * group][D] io_dt, dense, 16-byte aligned, written
+ *   lse       [total][heads_kv * group] fp32, written, or NULL
+ *   workspace >= dn_attn_workspace_bytes(...) bytes, 16-byte aligned, any contents; calls that may
+ *             run concurrently need separate ones
+ * Packed rows of no request are left unwritten. Keys and values that a row of the call sees, or that
+ * lie between those, are finite: probabilities of 0 still meet them in a product. What lies past
+ * kv_len[b], or in pages that a request does not name, may be anything. Scores, maxima, sums and
+ * outputs are kept in 32 bits; probabilities are rounded to 16 bits for the product with the
+ * values. The order of all sums is fixed by the sizes and lengths: results repeat bit for bit.
+ *
+ * dn_attn_workspace_bytes is 0 for sizes that dn_attn_paged refuses, B = 0 or total = 0.
+ */
+size_t dn_attn_workspace_bytes(int B, int total, int heads_kv, int group, int D);
+dn_status dn_attn_paged(int B, int total, int heads_kv, int group, int D, int page, int max_pages,
+                        int pages, dn_dtype io_dt, dn_dtype cache_dt, const void *q, int64_t q_stride,
+                        const int32_t *start, const int32_t *kv_len, const int32_t *page_table,
+                        const void *k_cache, const void *v_cache, const uint8_t *k_exp,
+                        const uint8_t *v_exp, float scale, int window, void *out, float *lse,
+                        void *workspace, size_t workspace_bytes, dn_stream_t stream);
 
 /* Static, NUL-terminated description of a status code. */
 const char *dn_status_string(dn_status s);

@@ -50,3 +50,4 @@ from .recurrence import (  # noqa: F401
 )
 from .accept import argmax_lowest, accept_greedy  # noqa: F401
 from .context_lookup import context_drafts_row, context_drafts  # noqa: F401
+from .paged_cache import decode_e4m3, encode_e4m3, quantise, values, kv_append, kv_gather, attn_paged  # noqa: F401
