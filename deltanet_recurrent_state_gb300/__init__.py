@@ -18,7 +18,7 @@ _API = (
     # paged cache of the attention layers: write, read back, attend
     "dn_kv_append", "dn_kv_gather", "dn_attn_paged", "dn_attn_workspace_bytes", "attn_workspace",
     # bounded-wait diagnostics
-    "dn_prefill_wait_timeouts", "dn_wait_selftest",
+    "dn_prefill_wait_timeouts", "dn_attn_wait_timeouts", "dn_wait_selftest",
     # errors and loading
     "dn_status_string", "DnError", "load_library",
 )

@@ -50,6 +50,7 @@ SIGNATURES = {
     "dn_kv_gather": (_I, [_I] * 9 + [_P] * 10),
     "dn_attn_workspace_bytes": (_S, [_I] * 5),
     "dn_attn_paged": (_I, [_I] * 10 + [_P, _L] + [_P] * 7 + [ctypes.c_float, _I, _P, _P, _P, _S, _P]),
+    "dn_attn_wait_timeouts": (ctypes.c_uint, []),
     "dn_context_drafts": (_I, [_I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
 }
 
@@ -413,6 +414,10 @@ def dn_attn_paged(q, start, kv_len, page_table, k_cache, v_cache, k_exp=None, v_
         workspace.numel() * workspace.element_size(), _stream(stream))
     _check("dn_attn_paged", st)
     return out, lse
+
+
+def dn_attn_wait_timeouts():
+    return int(load_library().dn_attn_wait_timeouts())
 
 
 class PrefixCache:

@@ -525,14 +525,15 @@ attn_join_kernel(const __grid_constant__ AttnArgs a, bool bf) {
 // ---- host: which kernel, and how many units ---------------------------------------------------
 
 struct AttnPlan {
+    bool tc;
     int M, target, align, min_range;
 };
 
 AttnPlan attn_plan(int B, int total, int G, int D) {
     // rows of a request, on average over the batch
     const long long rows = B > 0 ? ((long long)total * G + B - 1) / B : 0;
-    const int M = rows <= 16 || D == 256 ? 16 : 32;
-    return {M, 4 * kAttnSms, 64, 256};
+    if (rows > (D == 256 ? 16 : 32)) return {true, D == 256 ? 128 : 256, kAttnSms, D == 256 ? 64 : 128, 512};
+    return {false, rows <= 16 ? 16 : 32, 4 * kAttnSms, 64, 256};
 }
 
 template <int D, int MT, bool BF, bool KV8>
@@ -588,7 +589,8 @@ extern "C" dn_status dn_attn_paged(int B, int total, int heads_kv, int group, in
         !out || !workspace || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16) ||
         workspace_bytes < dn_attn_workspace_bytes(B, total, heads_kv, group, D))
         return DN_ERR_INVALID_ARG;
-    const AttnPlan p = attn_plan(B, total, group, D);
+    AttnPlan p = attn_plan(B, total, group, D);
+    if (pages == 0 || max_pages == 0) p = {false, 16, kAttnSms, 64, 256};  // nothing is cached: no pool to copy from
     const long long units = attn_units_bound(B, total, heads_kv, group, p.M, p.target);
     if (units > 0x7fffffffLL) return DN_ERR_INVALID_ARG;
     AttnArgs a;
@@ -611,7 +613,10 @@ extern "C" dn_status dn_attn_paged(int B, int total, int heads_kv, int group, in
     a.min_range = p.min_range;
     const bool bf = io_dt == DN_BF16, kv8 = cache_dt == DN_E4M3;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-    if (D == 64 && p.M == 16) launch_rows<64, 1>(a, bf, kv8, (unsigned)units, st);
+    if (p.tc && pages > 0 && max_pages > 0) {
+        const dn_status ok = launch_attn_tc(a, D, bf, kv8, (unsigned)units, st);
+        if (ok != DN_OK) return ok;
+    } else if (D == 64 && p.M == 16) launch_rows<64, 1>(a, bf, kv8, (unsigned)units, st);
     else if (D == 64) launch_rows<64, 2>(a, bf, kv8, (unsigned)units, st);
     else if (D == 128 && p.M == 16) launch_rows<128, 1>(a, bf, kv8, (unsigned)units, st);
     else if (D == 128) launch_rows<128, 2>(a, bf, kv8, (unsigned)units, st);

@@ -18,6 +18,7 @@
 // (a request of span > C has fewer than 2 span / C ranges), whatever B and the lengths are.
 #pragma once
 
+#include "dn.h"
 #include "dn_device.cuh"
 #include "dn_kv.cuh"
 
@@ -138,6 +139,6 @@ __device__ __forceinline__ bool attn_unit(const AttnArgs &a, int idx, AttnUnit &
 // Entry of the join kernel (dn_attn.cu), shared by both attention kernels.
 void launch_attn_join(const AttnArgs &a, int D, bool bf, cudaStream_t st);
 // Tiles of 128 rows on tcgen05 (dn_attn_tc.cu).
-dn_status launch_attn_tc(AttnArgs a, int D, bool bf, bool kv8, cudaStream_t st);
+dn_status launch_attn_tc(const AttnArgs &a, int D, bool bf, bool kv8, unsigned grid, cudaStream_t st);
 
 }  // namespace dn

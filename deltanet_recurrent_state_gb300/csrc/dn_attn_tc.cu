@@ -1,0 +1,690 @@
+// dn_attn_paged for tiles of many rows, on tcgen05 tensor cores.
+//
+// The mathematics is in dn_attn.cu, the cutting of the work in dn_attn.cuh. A unit is one CTA that
+// has an SM's tensor memory to itself: S = Q K^T of 128 rows by BN cached tokens, P = exp2(S - m),
+// O += P V, with S, P and O in tensor memory and nothing but Q, K and V in shared memory.
+//
+// Steps and streams. Step j computes S into buffer j & 1; its softmax turns that buffer into P (16 bits,
+// in the same columns); P V is added to an accumulator. The tensor core runs S(0), S(1), then P V(j),
+// S(j + 2), .., so one step's softmax always has another step's products beside it. For D <= 128 the
+// even and the odd steps are two streams with a warpgroup and an accumulator each: if the unit has more
+// than 128 rows (a prompt's chunk) the streams are its two halves of rows over the same keys, else
+// (a verify block) they are the even and the odd key tiles of the same rows, merged at the end. For D = 256
+// an accumulator takes half of the tensor memory: one stream, key tiles of 64 tokens.
+//
+// Copies. K and V tiles pass through one ring of shared-memory slots in the order in which the products take
+// them. Pages come in by TMA, one box per page and 64 columns, with the 128-byte swizzle that the MMA
+// descriptors read; each lane of the producer warp looks up and copies a box of its own. A page that a
+// request does not have is an out-of-range coordinate, which the copy fills with zeros. Rows of the last
+// page past the range may hold anything: their scores are masked, and their values are zeroed in
+// shared memory before the product (0 x NaN is not 0). For an 8-bit cache the boxes land in a ring of
+// raw tiles, and a warpgroup turns them into fp16 tiles (exact; the exponents go to the scores
+// and probabilities as in dn_attn.cu, with 2^7 in the place of 2^15, see below).
+//
+// Running maximum. O is rescaled only when a row's maximum grows by more than 2^8: until then its
+// probabilities are at most 2^8, exact in 16 bits as before, and the division by the sum at the end
+// takes the factor out again. With the 2^7 of an 8-bit cache's values they stay below fp16's 2^16.
+//
+// Every wait is bounded in time; a wait that runs out raises the CTA's abort flag, and every role
+// leaves after its own copies and products have landed.
+#include <type_traits>
+
+#include <cuda_runtime.h>
+
+#include "dn.h"
+#include "dn_attn.cuh"
+#include "dn_internal.h"
+#include "dn_mma.cuh"
+#include "dn_tc05.cuh"
+#include "dn_tmap.h"
+
+namespace dn {
+namespace {
+
+__device__ unsigned int g_attn_timeouts;
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// D += A B with A in tensor memory (16-bit elements, two to a column).
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n"
+                 :: "r"(d_tmem), "r"(a_tmem), "l"(b), "r"(idesc), "r"((uint32_t)acc) : "memory");
+}
+
+#define DN_R32(r)                                                                                                  \
+    "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),    \
+        "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),     \
+        "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),    \
+        "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+
+// 32 lanes x 32 columns; the registers may be read after tmem_wait_ld.
+__device__ __forceinline__ void tmem_ld32_start(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+                 "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+                   "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+                   "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+                   "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+                   "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+                 : "r"(taddr));
+}
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[N][32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : DN_R32(r[0])::"memory");
+#pragma unroll
+    for (int i = 1; i < N; ++i) asm volatile("" : DN_R32(r[i])::"memory");
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+                 "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+                 :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+                    "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+                    "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+                    "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+                 :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+                    "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tma_load_3d(void *smem, const void *tmap, int c0, int c1, int c2, unsigned long long *mb) {
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4}], [%5];"
+                 :: "r"(smem_addr(smem)), "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(mb)) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive(unsigned long long *mb) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_addr(mb)) : "memory");
+}
+__device__ __forceinline__ bool mbar_test(unsigned long long *mb, unsigned parity) {
+    unsigned ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}"
+                 : "=r"(ok) : "r"(smem_addr(mb)), "r"(parity) : "memory");
+    return ok;
+}
+// mbar_wait_guarded for a whole warp, which sees one answer; the timer is read only if the phase is not
+// complete at once.
+__device__ __forceinline__ bool wait_for(unsigned long long *mb, unsigned parity, volatile int *abort) {
+    bool ok = mbar_test(mb, parity);
+    if (__all_sync(0xffffffffu, ok)) return true;
+    if (!ok) ok = mbar_wait_guarded(mb, parity, abort, &g_attn_timeouts);
+    return __all_sync(0xffffffffu, ok);
+}
+
+template <int D, bool KV8>
+struct TileShape {
+    static constexpr int NS = D <= 128 ? 2 : 1;      // streams
+    static constexpr int BN = D <= 128 ? 128 : 64;   // tokens of a key tile
+    static constexpr int HALVES = D / 64;            // 64-column boxes of a tile
+    static constexpr int M = 128 * NS;               // rows of a unit
+    static constexpr int TILE = BN * D * 2;          // bytes of a 16-bit K or V tile
+    static constexpr int QTILE = 128 * D * 2;
+    static constexpr int SLOTS = KV8 ? (D == 64 ? 4 : 3) : (D == 64 ? 8 : 5);
+    static constexpr int RAW = KV8 ? BN * D : 0;     // bytes of an 8-bit tile
+    static constexpr int RAWS = KV8 ? (D == 64 ? 4 : 3) : 0;
+    static constexpr int SOFTMAX = 128 * NS;         // threads of the softmax warpgroups
+    static constexpr int THREADS = SOFTMAX + 128 + (KV8 ? 128 : 0);
+    static constexpr int OFF_RING = NS * QTILE;
+    static constexpr int OFF_RAW = OFF_RING + SLOTS * TILE;
+    static constexpr int OFF_SCALE = OFF_RAW + RAWS * RAW;                    // [4][2][BN] floats (8 bits)
+    static constexpr int OFF_ROW = OFF_SCALE + (KV8 ? 4 * 2 * BN * 4 : 0);    // [M] row factors
+    static constexpr int OFF_BAR = OFF_ROW + M * 4;
+    static constexpr int BYTES = OFF_BAR + 512 + 1024;                        // and the alignment of the base
+    static_assert(BYTES <= 232448, "shared memory of one CTA");
+    static_assert(NS == 1 || 128 * (D + 4) * 4 + 1024 <= SLOTS * TILE, "the streams merge in the ring");
+};
+
+struct Bars {
+    unsigned long long full[8], empty[8], raw_full[4], raw_empty[4], scale_full[4], s_full[2], p_full[2], pv, q_full, fin;
+    uint32_t tmem;
+    int abort, ref[4];
+};
+static_assert(sizeof(Bars) <= 512, "barriers");
+
+// Place of K (or V) tile t of n in the ring's order, and the other way round.
+__device__ __forceinline__ int seq_k(bool two_q, int t) { return two_q ? 2 * t : (t == 0 ? 0 : 2 * t - 1); }
+__device__ __forceinline__ int seq_v(bool two_q, int t, int n) { return two_q ? 2 * t + 1 : min(2 * t + 2, 2 * n - 1); }
+__device__ __forceinline__ void seq_tile(bool two_q, int seq, int n, int &t, bool &is_v) {
+    if (two_q) {
+        t = seq >> 1;
+        is_v = seq & 1;
+    } else {
+        is_v = seq == 2 * n - 1 || (seq > 0 && !(seq & 1));
+        t = seq == 2 * n - 1 ? n - 1 : (seq & 1) ? (seq + 1) >> 1 : seq == 0 ? 0 : (seq - 2) >> 1;
+    }
+}
+
+template <int D, bool BF, bool KV8>
+__global__ void __launch_bounds__(TileShape<D, KV8>::THREADS, 1)
+attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap mk,
+                 const __grid_constant__ CUtensorMap mv, bool io_bf) {
+    using S = TileShape<D, KV8>;
+    constexpr int BN = S::BN, NS = S::NS, SLOTS = S::SLOTS, TILE = S::TILE;
+    constexpr bool MB = BF && !KV8;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    unsigned char *ring = smem + S::OFF_RING, *raw = smem + S::OFF_RAW;
+    float *scales = reinterpret_cast<float *>(smem + S::OFF_SCALE);
+    float *row_factor = reinterpret_cast<float *>(smem + S::OFF_ROW);
+    Bars &bar = *reinterpret_cast<Bars *>(smem + S::OFF_BAR);
+    const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+    grid_dep_wait();
+    grid_dep_trigger();
+    AttnUnit u;
+    if (!attn_unit<false>(a, blockIdx.x, u)) return;
+    if (u.c >= u.ranges) return;
+    const int rows = (int)min((long long)S::M, (long long)u.n * a.G - (long long)u.t * S::M);
+    const bool two_q = NS == 2 && rows > 128;
+    const int tiles = (u.hi - u.lo + BN - 1) / BN;
+    const int steps = two_q ? 2 * tiles : tiles;
+    constexpr int W_TMA = S::SOFTMAX / 32, W_MMA = W_TMA + 1;
+
+    if (warp == W_MMA) tmem_alloc<512>(&bar.tmem);
+    if (tid == 0) {
+        for (int i = 0; i < SLOTS; ++i) {
+            mbar_init(&bar.full[i], KV8 ? 128 : 1);
+            mbar_init(&bar.empty[i], 1);
+        }
+        for (int i = 0; i < S::RAWS; ++i) {
+            mbar_init(&bar.raw_full[i], 1);
+            mbar_init(&bar.raw_empty[i], 128);
+        }
+        for (int i = 0; i < 4; ++i) mbar_init(&bar.scale_full[i], 128);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bar.s_full[i], 1);
+            mbar_init(&bar.p_full[i], 128);
+        }
+        mbar_init(&bar.pv, 1);
+        mbar_init(&bar.q_full, S::SOFTMAX);
+        mbar_init(&bar.fin, 1);
+        bar.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_proxy_async();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = bar.tmem;
+    volatile int *abort = &bar.abort;
+
+    if (warp == W_TMA) {
+        if (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        // ---- producer: a lane per box
+        const int page = 1 << a.p.page_shift, R = min(page, BN), H2 = KV8 ? 1 : S::HALVES;
+        const int boxes = BN / R * H2, sub = lane / H2, half = lane % H2;
+        constexpr int NB = KV8 ? S::RAWS : SLOTS;
+        int issued = 0;
+        auto look = [&](int t) {
+            const int j = u.lo + t * BN + sub * R;
+            const int pg = lane < boxes && j < u.hi ? pool_page(a.p, u.b, j) : -1;
+            return pg < 0 ? a.p.pages : pg;  // past the last page: zeros
+        };
+        int t;
+        bool is_v;
+        seq_tile(two_q, 0, tiles, t, is_v);
+        int pg = tiles > 0 ? look(t) : 0;
+        for (int seq = 0; seq < 2 * tiles; ++seq) {
+            seq_tile(two_q, seq, tiles, t, is_v);
+            const int slot = seq % NB, j0 = u.lo + t * BN;
+            unsigned long long *full = KV8 ? &bar.raw_full[slot % 4] : &bar.full[slot];
+            unsigned long long *empty = KV8 ? &bar.raw_empty[slot % 4] : &bar.empty[slot];
+            if (seq >= NB && !wait_for(empty, ((seq / NB) - 1) & 1, abort)) break;
+            if (lane == 0) mbar_arrive_expect_tx(full, KV8 ? S::RAW : TILE);
+            __syncwarp();
+            if (lane < boxes) {
+                unsigned char *dst = KV8 ? raw + slot * S::RAW + sub * R * D : ring + slot * TILE + half * BN * 128 + sub * R * 128;
+                tma_load_3d(dst, is_v ? &mv : &mk, half * 64, u.h * page + ((j0 + sub * R) & (page - 1)), pg, full);
+            }
+            issued = seq + 1;
+            if (seq + 1 < 2 * tiles) {
+                int t2;
+                bool v2;
+                seq_tile(two_q, seq + 1, tiles, t2, v2);
+                pg = look(t2);
+            }
+        }
+        if (*abort)  // what was copied has to land before the CTA leaves
+            for (int seq = max(0, issued - NB); seq < issued; ++seq)
+                mbar_drain(KV8 ? &bar.raw_full[seq % NB % 4] : &bar.full[seq % NB], (seq / NB) & 1);
+    } else if (warp == W_MMA) {
+        if (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        // ---- products
+        constexpr uint32_t type = MB ? (1u << 7) | (1u << 10) : 0u;
+        constexpr uint32_t id_s = umma_idesc(128, BN, 0, 0) | type, id_o = umma_idesc(128, D, 0, 1) | type;
+        bool ok = steps == 0 || wait_for(&bar.q_full, 0, abort);
+        tc_fence_after();
+        auto scores = [&](int j) {
+            const int t = two_q ? j >> 1 : j, seq = seq_k(two_q, t), slot = seq % SLOTS;
+            if (!wait_for(&bar.full[slot], (seq / SLOTS) & 1, abort)) return false;
+            tc_fence_after();
+            if (lane == 0) {
+                const uint32_t qa = smem_addr(smem) + (two_q ? (j & 1) * S::QTILE : 0), ka = smem_addr(ring) + slot * TILE;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    umma_f16(tm + (j & 1) * BN, desc_kmajor(qa + (k / 4) * 128 * 128 + (k % 4) * 32),
+                             desc_kmajor(ka + (k / 4) * BN * 128 + (k % 4) * 32), id_s, k > 0);
+                if (!two_q || (j & 1)) umma_commit(&bar.empty[slot]);
+                umma_commit(&bar.s_full[j & 1]);
+            }
+            __syncwarp();
+            return true;
+        };
+        auto outputs = [&](int j) {
+            const int t = two_q ? j >> 1 : j, seq = seq_v(two_q, t, tiles), slot = seq % SLOTS;
+            if (!wait_for(&bar.full[slot], (seq / SLOTS) & 1, abort)) return false;
+            const int live = u.hi - (u.lo + t * BN);
+            if (!KV8 && live < BN && (!two_q || !(j & 1))) {
+                // values past the range
+                for (int i = lane; i < (BN - live) * 8 * S::HALVES; i += 32) {
+                    const int r = live + i / (8 * S::HALVES), c = i % (8 * S::HALVES);
+                    *reinterpret_cast<uint4 *>(ring + slot * TILE + (c / 8) * BN * 128 + r * 128 + (c % 8) * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async();
+                __syncwarp();
+            }
+            if (!wait_for(&bar.p_full[j & 1], (j >> 1) & 1, abort)) return false;
+            tc_fence_after();
+            if (lane == 0) {
+                const uint32_t va = smem_addr(ring) + slot * TILE, o = tm + 256 + (NS == 2 ? (j & 1) * 128 : 0);
+#pragma unroll
+                for (int k = 0; k < BN / 16; ++k)
+                    umma_ts(o, tm + (j & 1) * BN + 8 * k, desc_mnmajor(va + k * 2048, BN * 128), id_o, k > 0 || j >= NS);
+                if (!two_q || (j & 1)) umma_commit(&bar.empty[slot]);
+                if (D != 128) umma_commit(&bar.pv);
+            }
+            __syncwarp();
+            // S(j + 2) overwrites P(j): products of one shape follow each other in order, of two shapes
+            // (D other than 128) the overwriting one is issued after the reading one is complete
+            if (D != 128 && j + 2 < steps && !wait_for(&bar.pv, j & 1, abort)) return false;
+            return true;
+        };
+        if (ok && steps > 0) ok = scores(0);
+        if (ok && steps > 1) ok = scores(1);
+        for (int j = 0; ok && j < steps; ++j) {
+            ok = outputs(j);
+            if (ok && j + 2 < steps) ok = scores(j + 2);
+        }
+        if (steps > 0 && lane == 0) umma_commit(&bar.fin);
+        __syncwarp();
+        if (!ok) mbar_drain(&bar.fin, 0);
+    } else if (warp >= W_TMA && warp < W_TMA + 4) {
+        if (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    } else if (KV8 && warp >= W_TMA + 4) {
+        if (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        // ---- 8-bit tiles to fp16
+        const int c = tid - (W_TMA + 4) * 32;
+        int ref = 0;
+        for (int seq = 0; seq < 2 * tiles; ++seq) {
+            int t;
+            bool is_v;
+            seq_tile(two_q, seq, tiles, t, is_v);
+            const int j0 = u.lo + t * BN, live = min(BN, u.hi - j0);
+            // exponents of tokens 4 lane .. + 3, by every warp for itself (in the shadow of the waits)
+            unsigned ek = 0, ev = 0;
+            if (!is_v && 4 * lane < live) {
+                const int pg = pool_page(a.p, u.b, j0 + 4 * lane);
+                if (pg >= 0) {
+                    const long long at = ((((long long)pg * a.p.heads + u.h)) << a.p.page_shift) + ((j0 + 4 * lane) & ((1 << a.p.page_shift) - 1));
+                    ek = __ldg(reinterpret_cast<const unsigned *>(a.ke + at));
+                    ev = __ldg(reinterpret_cast<const unsigned *>(a.ve + at));
+                    if (live - 4 * lane < 4) {  // bytes past the range are not the request's
+                        const unsigned mask = (1u << (8 * (live - 4 * lane))) - 1u;
+                        ek &= mask;
+                        ev &= mask;
+                    }
+                }
+            }
+            const int slot = seq % SLOTS, rs = seq % (KV8 ? S::RAWS : 1);
+            if (seq >= SLOTS && !wait_for(&bar.empty[slot], ((seq / SLOTS) - 1) & 1, abort)) break;
+            if (!wait_for(&bar.raw_full[rs], (seq / (KV8 ? S::RAWS : 1)) & 1, abort)) break;
+            if (!is_v) {
+                // factors of the tile's scores and probabilities; the largest value exponent so far
+                unsigned top = __vmaxu4(ev, ev >> 16);
+                top = __reduce_max_sync(0xffffffffu, max(top & 0xffu, (top >> 8) & 0xffu));
+                ref = max(ref, (int)top);
+                if (lane / 8 == warp % 4 && 4 * lane < BN) {  // each warp writes 32 tokens
+                    float *kf = scales + (t & 3) * 2 * BN + 4 * lane;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        kf[e] = exp_byte((ek >> (8 * e)) & 0xffu);
+                        const int x = (int)((ev >> (8 * e)) & 0xffu) - ref + 7 + 127;
+                        kf[BN + e] = 4 * lane + e < live ? __int_as_float(max(x, 0) << 23) : 0.f;
+                    }
+                }
+                if (c == 0) bar.ref[t & 3] = ref;
+                mbar_arrive(&bar.scale_full[t & 3]);
+            }
+            const unsigned char *src = raw + rs * S::RAW;
+            unsigned char *dst = ring + slot * TILE;
+#pragma unroll 4
+            for (int i = 0; i < BN * D / 16 / 128; ++i) {
+                const int x = i * 128 + c, r = x / (D / 16), e = x % (D / 16) * 16, half = e / 64, ch = e % 64 / 8;
+                uint4 w = *reinterpret_cast<const uint4 *>(src + x * 16);
+                if (r >= live) w = make_uint4(0, 0, 0, 0);
+                uint4 o[2];
+                o[0] = make_uint4(unpack_e4m3((unsigned short)w.x), unpack_e4m3((unsigned short)(w.x >> 16)),
+                                  unpack_e4m3((unsigned short)w.y), unpack_e4m3((unsigned short)(w.y >> 16)));
+                o[1] = make_uint4(unpack_e4m3((unsigned short)w.z), unpack_e4m3((unsigned short)(w.z >> 16)),
+                                  unpack_e4m3((unsigned short)w.w), unpack_e4m3((unsigned short)(w.w >> 16)));
+                unsigned char *row = dst + half * BN * 128 + r * 128;
+                const int first = half & 1;  // lanes of neighbouring halves store to different banks
+                *reinterpret_cast<uint4 *>(row + (((ch + first) ^ (r & 7)) << 4)) = first ? o[1] : o[0];
+                *reinterpret_cast<uint4 *>(row + (((ch + 1 - first) ^ (r & 7)) << 4)) = first ? o[0] : o[1];
+            }
+            fence_proxy_async();
+            mbar_arrive(&bar.full[slot]);
+            mbar_arrive(&bar.raw_empty[rs]);
+        }
+    } else {
+        // ---- softmax: a thread per row
+        if (NS == 2) {
+            if (KV8) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+            else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        }
+        const int s = warp / 4, row = tid % 128;
+        // q to shared memory, K-major with the 128-byte swizzle; rows that are not there are zeros
+        if (!KV8) {
+            for (int x = tid; x < (two_q ? 256 : 128) * (D / 8); x += S::SOFTMAX) {
+                const int r = x / (D / 8), c = x % (D / 8);
+                uint4 w = make_uint4(0, 0, 0, 0);
+                if (r < rows) {
+                    const long long rr = (long long)u.t * S::M + r;
+                    w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(a.q) + (u.s + rr / a.G) * a.q_stride +
+                                                              (u.h * a.G + rr % a.G) * D) + c);
+                }
+                *reinterpret_cast<uint4 *>(smem + (r / 128) * S::QTILE + (c / 8) * 128 * 128 + (r % 128) * 128 + (((c % 8) ^ (r & 7)) << 4)) = w;
+            }
+        } else if (two_q || tid < 128) {
+            // fp16 by a power of two for each row, as in dn_attn.cu
+            const bool live = tid < rows;
+            const long long rr = (long long)u.t * S::M + tid;
+            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(a.q) + (live ? (u.s + rr / a.G) * a.q_stride +
+                                                               (u.h * a.G + rr % a.G) * D : 0));
+            float big = 0.f;
+            for (int c = 0; c < D / 8; ++c) {
+                const uint4 w = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+                const unsigned v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = io_bf ? unpack2<true>(v[e]) : unpack2<false>(v[e]);
+                    big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
+                }
+            }
+            const int e2 = min(max((int)(__float_as_uint(big) >> 23) - 127, -126), 126);
+            const float f2 = __int_as_float((127 - e2) << 23);
+            row_factor[tid] = a.scale_log2 * __int_as_float((127 + e2) << 23);
+            for (int c = 0; c < D / 8; ++c) {
+                const uint4 w = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+                unsigned v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 f = io_bf ? unpack2<true>(v[e]) : unpack2<false>(v[e]);
+                    v[e] = pack2<false>(f.x * f2, f.y * f2);
+                }
+                *reinterpret_cast<uint4 *>(smem + (tid / 128) * S::QTILE + (c / 8) * 128 * 128 + row * 128 + (((c % 8) ^ (row & 7)) << 4)) =
+                    make_uint4(v[0], v[1], v[2], v[3]);
+            }
+        }
+        fence_proxy_async();
+        mbar_arrive(&bar.q_full);
+        if (KV8) bar_sync(1, S::SOFTMAX);  // row_factor
+        const int r_unit = two_q ? s * 128 + row : row;  // this thread's row of the unit
+        const float factor = KV8 ? row_factor[r_unit] : a.scale_log2;
+        const long long r_all = (long long)u.t * S::M + r_unit;
+        const int pos = u.first + (int)(r_all / a.G);
+        // positions of the first and last row of the stream, for whole tiles without a mask
+        const int r_first = two_q ? s * 128 : 0;
+        const int pos_first = u.first + (int)(((long long)u.t * S::M + r_first) / a.G);
+        const int pos_last = u.first + (int)(((long long)u.t * S::M + r_first + 127) / a.G);
+        const uint32_t lanes = (uint32_t)(32 * (warp % 4)) << 16;
+        const uint32_t o_addr = tm + lanes + 256 + (NS == 2 ? s * 128 : 0);
+        float m = -INFINITY, l = 0.f;
+        int ref = 0;
+        bool ok = true, any = false;
+        for (int j = NS == 2 ? s : 0; j < steps; j += NS) {
+            const int t = two_q ? j >> 1 : j, j0 = u.lo + t * BN;
+            const uint32_t s_addr = tm + lanes + (j & 1) * BN;
+            if (!wait_for(&bar.s_full[j & 1], (j >> 1) & 1, abort)) { ok = false; break; }
+            tc_fence_after();
+            uint32_t x[BN / 32][32];
+#pragma unroll
+            for (int i = 0; i < BN / 32; ++i) tmem_ld32_start(s_addr + 32 * i, x[i]);
+            const float *kf = scales + (t & 3) * 2 * BN, *vf = kf + BN;
+            int ref_now = 0;
+            if (KV8) {
+                if (!wait_for(&bar.scale_full[t & 3], (t >> 2) & 1, abort)) { ok = false; break; }
+                ref_now = bar.ref[t & 3];
+            }
+            tmem_wait_ld(x);
+            if (KV8) {
+#pragma unroll
+                for (int i = 0; i < BN; i += 4) {
+                    const float4 f = *reinterpret_cast<const float4 *>(kf + i);
+                    x[i / 32][i % 32] = __float_as_uint(__uint_as_float(x[i / 32][i % 32]) * f.x);
+                    x[i / 32][i % 32 + 1] = __float_as_uint(__uint_as_float(x[i / 32][i % 32 + 1]) * f.y);
+                    x[i / 32][i % 32 + 2] = __float_as_uint(__uint_as_float(x[i / 32][i % 32 + 2]) * f.z);
+                    x[i / 32][i % 32 + 3] = __float_as_uint(__uint_as_float(x[i / 32][i % 32 + 3]) * f.w);
+                }
+            }
+            if (j0 + BN - 1 > pos_first || j0 + BN > u.hi || (a.window && j0 <= pos_last - a.window)) {
+                const int most = min(pos, u.hi - 1) - j0, least = a.window ? pos - a.window - j0 : -1;
+#pragma unroll
+                for (int i = 0; i < BN; ++i)
+                    if (i > most || i <= least) x[i / 32][i % 32] = 0xff800000u;  // -inf
+            }
+            float b0 = -INFINITY, b1 = -INFINITY, b2 = -INFINITY, b3 = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < BN; i += 4) {
+                b0 = fmaxf(b0, __uint_as_float(x[i / 32][i % 32]));
+                b1 = fmaxf(b1, __uint_as_float(x[i / 32][i % 32 + 1]));
+                b2 = fmaxf(b2, __uint_as_float(x[i / 32][i % 32 + 2]));
+                b3 = fmaxf(b3, __uint_as_float(x[i / 32][i % 32 + 3]));
+            }
+            const float big = fmaxf(fmaxf(b0, b1), fmaxf(b2, b3)) * factor;
+            if (!any) {
+                any = true;
+                m = big;
+                ref = ref_now;
+            } else {
+                const bool grew = big > m + 8.f;
+                const float base_old = m;
+                if (grew) m = big;
+                float f = grew ? ex2(base_old - m) : 1.f;
+                const bool moved = KV8 && ref_now != ref;
+                if (__any_sync(0xffffffffu, grew) || moved) {
+                    l *= f;
+                    if (moved) f *= ex2((float)(ref - ref_now));
+                    ref = ref_now;
+                    if (NS == 1) {  // the product of the step before may be under way
+                        if (!wait_for(&bar.pv, (j - 1) & 1, abort)) { ok = false; break; }
+                        tc_fence_after();
+                    }
+#pragma unroll 1
+                    for (int d = 0; d < D; d += 32) {
+                        uint32_t y[1][32];
+                        tmem_ld32_start(o_addr + d, y[0]);
+                        tmem_wait_ld(y);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) y[0][e] = __float_as_uint(__uint_as_float(y[0][e]) * f);
+                        tmem_st32(o_addr + d, y[0]);
+                    }
+                }
+            }
+            const float base = m == -INFINITY ? 0.f : m;
+            float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+            for (int i = 0; i < BN / 32; ++i) {
+                uint32_t p[16];
+#pragma unroll
+                for (int e = 0; e < 32; e += 2) {
+                    float p0 = ex2(fmaf(__uint_as_float(x[i][e]), factor, -base)), p1 = ex2(fmaf(__uint_as_float(x[i][e + 1]), factor, -base));
+                    l0 += p0;
+                    l1 += p1;
+                    if (KV8) {
+                        const float2 f = *reinterpret_cast<const float2 *>(vf + 32 * i + e);
+                        p0 *= f.x;
+                        p1 *= f.y;
+                    }
+                    p[e / 2] = pack2<MB>(p0, p1);
+                }
+                tmem_st16(s_addr + 16 * i, p);
+            }
+            l += l0 + l1;
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&bar.p_full[j & 1]);
+        }
+        // ---- the outputs (tensor-memory loads are the whole warp's, stores each row's own)
+        if (steps > 0 && ok) ok = wait_for(&bar.fin, 0, abort);
+        tc_fence_after();
+        const float unit = KV8 ? ex2((float)(ref - 127 - 7)) : 1.f;
+        constexpr int PITCH = D + 4;
+        float *mo = reinterpret_cast<float *>(ring);
+        float2 *ml = reinterpret_cast<float2 *>(ring + 128 * PITCH * 4);
+        const bool merge = NS == 2 && !two_q;
+        if (merge) {
+            if (ok && s == 1) {
+                ml[row] = make_float2(m, l);
+#pragma unroll 1
+                for (int d = 0; any && d < D; d += 32) {
+                    uint32_t y[1][32];
+                    tmem_ld32_start(o_addr + d, y[0]);
+                    tmem_wait_ld(y);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4 *>(mo + row * PITCH + d + e) =
+                            make_float4(__uint_as_float(y[0][e]) * unit, __uint_as_float(y[0][e + 1]) * unit,
+                                        __uint_as_float(y[0][e + 2]) * unit, __uint_as_float(y[0][e + 3]) * unit);
+                }
+            }
+            bar_sync(2, 256);
+        }
+        if (ok && !(merge && s == 1) && __any_sync(0xffffffffu, r_unit < rows)) {
+            const bool live = r_unit < rows, other = merge && tiles > 1;  // (stream 1 has a tile of its own)
+            float top = m, f0 = unit, f1 = 0.f, sum = l;
+            if (other) {
+                const float2 y = ml[row];
+                top = fmaxf(m, y.x);
+                const float base = top == -INFINITY ? 0.f : top;
+                f0 = ex2(m - base);
+                f1 = ex2(y.x - base);
+                sum = f0 * l + f1 * y.y;
+                f0 *= unit;
+            }
+            const bool final = u.ranges == 1;
+            if (final) {
+                const float inv = sum > 0.f ? 1.f / sum : sum != sum ? sum : 0.f;  // NaN stays NaN
+                f0 *= inv;
+                f1 *= inv;
+            }
+            const long long at = (u.s + r_all / a.G) * ((long long)a.p.heads * a.G) + u.h * a.G + r_all % a.G;
+            float *part = a.part + (size_t)(u.slot + u.c) * S::M * (D + 2);
+            const bool bf = KV8 ? io_bf : BF;
+#pragma unroll 1
+            for (int d = 0; d < D; d += 32) {
+                uint32_t y[1][32];
+                float z[32];
+                if (any) {
+                    tmem_ld32_start(o_addr + d, y[0]);
+                    tmem_wait_ld(y);
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e) z[e] = any ? f0 * __uint_as_float(y[0][e]) : 0.f;
+                if (other) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) {
+                        const float4 w = *reinterpret_cast<const float4 *>(mo + row * PITCH + d + e);
+                        z[e] = fmaf(f1, w.x, z[e]);
+                        z[e + 1] = fmaf(f1, w.y, z[e + 1]);
+                        z[e + 2] = fmaf(f1, w.z, z[e + 2]);
+                        z[e + 3] = fmaf(f1, w.w, z[e + 3]);
+                    }
+                }
+                if (live && final) {
+                    unsigned short *dst = static_cast<unsigned short *>(a.out) + at * D + d;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint4 w;
+                        w.x = bf ? pack2<true>(z[e], z[e + 1]) : pack2<false>(z[e], z[e + 1]);
+                        w.y = bf ? pack2<true>(z[e + 2], z[e + 3]) : pack2<false>(z[e + 2], z[e + 3]);
+                        w.z = bf ? pack2<true>(z[e + 4], z[e + 5]) : pack2<false>(z[e + 4], z[e + 5]);
+                        w.w = bf ? pack2<true>(z[e + 6], z[e + 7]) : pack2<false>(z[e + 6], z[e + 7]);
+                        *reinterpret_cast<uint4 *>(dst + e) = w;
+                    }
+                } else if (live) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4 *>(part + (size_t)r_unit * D + d + e) = make_float4(z[e], z[e + 1], z[e + 2], z[e + 3]);
+                }
+                __syncwarp();
+            }
+            if (live && final) {
+                if (a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945f;
+            } else if (live) {
+                *reinterpret_cast<float2 *>(part + (size_t)S::M * D + 2 * r_unit) = make_float2(top, sum);
+            }
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == W_MMA) tmem_free<512>(tm);
+}
+
+// [pages][heads * page][D] of a pool: boxes of 64 columns with the 128-byte swizzle (16-bit), or whole
+// rows without (8-bit), min(page, BN) rows high.
+bool pool_map(CUtensorMap *m, const void *base, const AttnArgs &a, int D, int eb, int rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t page = 1ull << a.p.page_shift;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, a.p.heads * page, (cuuint64_t)a.p.pages};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * eb, a.p.heads * page * D * eb};
+    const cuuint32_t box[3] = {(cuuint32_t)(eb == 1 ? D : 64), (cuuint32_t)rows, 1}, es[3] = {1, 1, 1};
+    return enc(m, eb == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(base), dims, strides,
+               box, es, CU_TENSOR_MAP_INTERLEAVE_NONE, eb == 1 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool BF, bool KV8>
+dn_status launch_tile(const AttnArgs &a, bool io_bf, unsigned grid, cudaStream_t st) {
+    using S = TileShape<D, KV8>;
+    const int rows = 1 << a.p.page_shift < S::BN ? 1 << a.p.page_shift : S::BN;
+    CUtensorMap mk, mv;
+    if (!pool_map(&mk, a.kc, a, D, KV8 ? 1 : 2, rows) || !pool_map(&mv, a.vc, a, D, KV8 ? 1 : 2, rows)) return DN_ERR_CUDA;
+    cudaFuncSetAttribute(attn_tile_kernel<D, BF, KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
+    launch_pdl(attn_tile_kernel<D, BF, KV8>, dim3(grid), dim3(S::THREADS), S::BYTES, st, a, mk, mv, io_bf);
+    return DN_OK;
+}
+
+template <int D>
+dn_status launch_tile(const AttnArgs &a, bool bf, bool kv8, unsigned grid, cudaStream_t st) {
+    if (kv8) return launch_tile<D, false, true>(a, bf, grid, st);
+    return bf ? launch_tile<D, true, false>(a, bf, grid, st) : launch_tile<D, false, false>(a, bf, grid, st);
+}
+
+}  // namespace
+
+dn_status launch_attn_tc(const AttnArgs &a, int D, bool bf, bool kv8, unsigned grid, cudaStream_t st) {
+    if (D == 64) return launch_tile<64>(a, bf, kv8, grid, st);
+    if (D == 128) return launch_tile<128>(a, bf, kv8, grid, st);
+    return launch_tile<256>(a, bf, kv8, grid, st);
+}
+
+}  // namespace dn
+
+extern "C" unsigned int dn_attn_wait_timeouts(void) {
+    unsigned int v = 0;
+    if (cudaMemcpyFromSymbol(&v, dn::g_attn_timeouts, sizeof(v)) != cudaSuccess) {
+        cudaGetLastError();
+        return 0xffffffffu;
+    }
+    return v;
+}

@@ -492,6 +492,14 @@ dn_status dn_attn_paged(int B, int total, int heads_kv, int group, int D, int pa
                         const uint8_t *v_exp, float scale, int window, void *out, float *lse,
                         void *workspace, size_t workspace_bytes, dn_stream_t stream);
 
+/*
+ * dn_attn_wait_timeouts -- diagnostics of dn_attn_paged's kernel for many rows, as
+ * dn_prefill_wait_timeouts: how many CTAs gave up a bounded wait since the library was loaded on the
+ * current device (0 in correct operation; a call in which one did has invalid results, and nothing
+ * hangs), or 0xffffffff if the counter could not be read. Synchronises the current device.
+ */
+unsigned int dn_attn_wait_timeouts(void);
+
 /* Static, NUL-terminated description of a status code. */
 const char *dn_status_string(dn_status s);
 
