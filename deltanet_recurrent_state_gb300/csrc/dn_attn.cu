@@ -88,7 +88,7 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a, bool io_bf) {
     AttnUnit u;
     if (!attn_unit<false>(a, blockIdx.x, u)) return;
     if (u.c >= u.ranges) return;
-    const int rows = (int)min((long long)M, (long long)u.n * a.G - (long long)u.t * M);
+    const int row0 = u.t * M, rows = min(M, u.n * a.G - row0);  // (the host bounds total * heads)
 
     // ---- the ring: piece i of this warp is tokens lo + 16 (warp + W i) .. + 15 of the range
     unsigned char *ring = smem + (size_t)warp * ST * S::STAGE;
@@ -130,10 +130,9 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a, bool io_bf) {
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
             const int r = 16 * mt + g + 8 * hh;
-            const long long rr = (long long)u.t * M + r;
-            const int tok = (int)(rr / a.G);
-            src[hh] = r < rows ? static_cast<const unsigned short *>(a.q) + (u.s + (long long)tok) * a.q_stride +
-                                     (long long)(u.h * a.G + (int)(rr % a.G)) * D
+            const int tok = (row0 + r) / a.G;
+            src[hh] = r < rows ? static_cast<const unsigned short *>(a.q) + (u.s + tok) * a.q_stride +
+                                     (long long)(u.h * a.G + row0 + r - tok * a.G) * D
                                : nullptr;
             pos[mt][hh] = r < rows ? u.first + tok : -(1 << 30) - (1 << 29);
             row_scale[mt][hh] = a.scale_log2;
@@ -195,8 +194,8 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a, bool io_bf) {
         }
     }
     if (!S::QREG) __syncthreads();
-    const int row0_pos = u.first + (int)((long long)u.t * M / a.G);  // positions of the tile's first and last token
-    const int last = u.first + (int)(((long long)u.t * M + rows - 1) / a.G);
+    const int row0_pos = u.first + row0 / a.G;  // positions of the tile's first and last token
+    const int last = u.first + (row0 + rows - 1) / a.G;
 
     float o[MT][D / 8][4];
     float m[MT][2], l[MT][2];
@@ -429,8 +428,8 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a, bool io_bf) {
             acc.w = fmaf(f, v.w, acc.w);
         }
         if (final) {
-            const long long rr = (long long)u.t * M + r;
-            const long long at = (u.s + rr / a.G) * ((long long)a.p.heads * a.G) + u.h * a.G + rr % a.G;
+            const int tok = (row0 + r) / a.G;
+            const size_t at = (u.s + tok) * (a.p.heads * a.G) + u.h * a.G + row0 + r - tok * a.G;
             const float inv = sum > 0.f ? 1.f / sum : 0.f;
             if (sum != sum) acc.x = acc.y = acc.z = acc.w = sum;
             uint2 w;
@@ -462,7 +461,7 @@ attn_join_kernel(const __grid_constant__ AttnArgs a, bool bf) {
     grid_dep_trigger();
     AttnUnit u;
     if (!attn_unit<true>(a, blockIdx.x, u) || u.ranges < 2) return;
-    const int M = a.M, rows = (int)min((long long)M, (long long)u.n * a.G - (long long)u.t * M);
+    const int M = a.M, row0 = u.t * M, rows = min(M, u.n * a.G - row0);
     const int r = blockIdx.y * kJoinRows + (warp >> 1), half = warp & 1;
     if ((int)(blockIdx.y * kJoinRows) >= rows) return;
     float acc[E];
@@ -509,8 +508,8 @@ attn_join_kernel(const __grid_constant__ AttnArgs a, bool bf) {
     const float f0 = exp2_fast(top - base), f1 = exp2_fast(y.x - base);
     sum = f0 * sum + f1 * y.y;
     const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    const long long rr = (long long)u.t * M + r;
-    const long long at = (u.s + rr / a.G) * ((long long)a.p.heads * a.G) + u.h * a.G + rr % a.G;
+    const int tok = (row0 + r) / a.G;
+    const size_t at = (u.s + tok) * (a.p.heads * a.G) + u.h * a.G + row0 + r - tok * a.G;
     unsigned *dst = reinterpret_cast<unsigned *>(static_cast<unsigned short *>(a.out) + at * D + E * lane);
 #pragma unroll
     for (int e = 0; e < E; e += 2) {
@@ -581,7 +580,7 @@ extern "C" dn_status dn_attn_paged(int B, int total, int heads_kv, int group, in
         !(scale > 0.f) || scale > 3e38f || !kv_dtypes_known(io_dt, cache_dt))
         return DN_ERR_INVALID_ARG;
     if (!kv_shape_ok(D, page) || !kv_dtypes_ok(io_dt, cache_dt)) return DN_ERR_UNSUPPORTED;
-    if ((long long)heads_kv * group > (1 << 20) || (long long)total * heads_kv * group > 0x7fffffffLL ||
+    if ((long long)heads_kv * group > (1 << 20) || (long long)total * heads_kv * group > 0x7fffffffLL - 1024 ||
         !kv_pages_ok(max_pages, pages, page) || q_stride < (int64_t)heads_kv * group * D || q_stride % 8)
         return DN_ERR_INVALID_ARG;
     if (B == 0 || total == 0) return DN_OK;
@@ -606,7 +605,7 @@ extern "C" dn_status dn_attn_paged(int B, int total, int heads_kv, int group, in
     a.part = static_cast<float *>(workspace);
     a.G = group;
     a.scale_log2 = scale * 1.44269504088896f;
-    a.window = window > DN_KV_MAX_TOKENS ? 0 : window;
+    a.window = window >= DN_KV_MAX_TOKENS ? 0 : window;
     a.M = p.M;
     a.align = p.align;
     a.target = p.target;

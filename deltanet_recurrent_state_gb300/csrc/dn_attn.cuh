@@ -66,8 +66,8 @@ __device__ __forceinline__ void attn_request(const AttnArgs &a, int b, int &s, i
     const int held = min(max(__ldg(&a.p.kv_len[b]), 0), 1 << 30);
     first = held - n;
     len = min(held, a.p.max_pages << a.p.page_shift);
-    tiles = (int)(((long long)n * a.G + a.M - 1) / a.M);
-    span = a.window ? (int)min((long long)len, (long long)a.window + (a.M - 1) / a.G + 1 + a.align) : len;
+    tiles = (n * a.G + a.M - 1) / a.M;  // (the host bounds total * heads by 2^31 - 1 - M)
+    span = a.window ? min(len, a.window + (a.M - 1) / a.G + 1 + a.align) : len;  // (window <= 2^30)
 }
 
 // The unit with this number (JOIN: the tile and head with this number among those of requests with
@@ -83,14 +83,15 @@ __device__ __forceinline__ bool attn_unit(const AttnArgs &a, int idx, AttnUnit &
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) work += __shfl_xor_sync(0xffffffffu, work, off);
-    long long C = (work * a.p.heads + a.target - 1) / a.target;
-    C = max((C + a.align - 1) / a.align * a.align, (long long)a.min_range);
-    const int range = (int)min(C, 1ll << 30);
+    // C = work * heads / target, rounded up to a multiple of align: in 32 bits unless the work is huge
+    work = work * a.p.heads + a.target - 1;
+    const long long C = work < 0x7fffffff ? (int)work / a.target : work / a.target;
+    const int range = max((int)min((C + a.align - 1) / a.align * a.align, 1ll << 30), a.min_range);
     int before = 0, slots_before = 0;
     for (int i = 0; i < B; i += 32) {
         int s = 0, n = 0, first = 0, len = 0, tiles = 0, span = 0;
         if (i + lane < B) attn_request(a, i + lane, s, n, first, len, tiles, span);
-        const int ranges = max(1, (int)(((long long)span + range - 1) / range));
+        const int ranges = max(1, (span + range - 1) / range);  // (both at most 2^30)
         const int slots = ranges > 1 ? tiles * ranges * a.p.heads : 0;
         const int units = JOIN ? (ranges > 1 ? tiles * a.p.heads : 0) : tiles * ranges * a.p.heads;
         int upto = units, slots_upto = slots;
@@ -120,14 +121,13 @@ __device__ __forceinline__ bool attn_unit(const AttnArgs &a, int idx, AttnUnit &
             u.c = JOIN ? 0 : local % R;
             u.h = JOIN ? local : local / R;
             u.slot = slots_before + from(slots_upto - slots) + (u.h * T + u.t) * R;
-            const long long r0 = (long long)u.t * a.M, r1 = min(r0 + a.M, (long long)u.n * a.G);
-            const int i0 = (int)(r0 / a.G), i1 = (int)((r1 - 1) / a.G);
-            const int hi = min(max(u.first + i1 + 1, 0), u.len);
-            int lo = a.window ? max(u.first + i0 - a.window + 1, 0) : 0;
-            lo = min(lo / a.align * a.align, hi);
-            u.ranges = max(1, (int)(((long long)hi - lo + range - 1) / range));
-            u.lo = (int)min((long long)lo + (long long)u.c * range, (long long)hi);
-            u.hi = (int)min((long long)u.lo + range, (long long)hi);
+            const int r0 = u.t * a.M, r1 = min(a.M, u.n * a.G - r0) - 1 + r0;
+            const int hi = min(max(u.first + r1 / a.G + 1, 0), u.len);
+            int lo = a.window ? max(u.first + r0 / a.G - a.window + 1, 0) : 0;
+            lo = min(lo & ~(a.align - 1), hi);  // (align is a power of two)
+            u.ranges = max(1, (hi - lo + range - 1) / range);
+            u.lo = u.c < u.ranges ? lo + u.c * range : hi;
+            u.hi = hi - u.lo > range ? u.lo + range : hi;
             return true;
         }
         before += __shfl_sync(0xffffffffu, upto, 31);

@@ -118,6 +118,16 @@ __device__ __forceinline__ bool wait_for(unsigned long long *mb, unsigned parity
     if (!ok) ok = mbar_wait_guarded(mb, parity, abort, &g_attn_timeouts);
     return __all_sync(0xffffffffu, ok);
 }
+// The same for a single thread.
+__device__ __forceinline__ bool wait_one(unsigned long long *mb, unsigned parity, volatile int *abort) {
+    return mbar_test(mb, parity) || mbar_wait_guarded(mb, parity, abort, &g_attn_timeouts);
+}
+
+__device__ __forceinline__ bool elect_one() {
+    unsigned r;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(r));
+    return r;
+}
 
 template <int D, bool KV8>
 struct TileShape {
@@ -143,7 +153,7 @@ struct TileShape {
 };
 
 struct Bars {
-    unsigned long long full[8], empty[8], raw_full[4], raw_empty[4], scale_full[4], s_full[2], p_full[2], pv, q_full, fin;
+    unsigned long long full[8], empty[8], raw_full[4], raw_empty[4], scale_full[4], s_full[2], p_full[2], pv, q_full, last_v, fin;
     uint32_t tmem;
     int abort, ref[4];
 };
@@ -181,7 +191,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
     AttnUnit u;
     if (!attn_unit<false>(a, blockIdx.x, u)) return;
     if (u.c >= u.ranges) return;
-    const int rows = (int)min((long long)S::M, (long long)u.n * a.G - (long long)u.t * S::M);
+    const int row0 = u.t * S::M, rows = min(S::M, u.n * a.G - row0);  // (the host bounds total * heads)
     const bool two_q = NS == 2 && rows > 128;
     const int tiles = (u.hi - u.lo + BN - 1) / BN;
     const int steps = two_q ? 2 * tiles : tiles;
@@ -204,6 +214,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
         }
         mbar_init(&bar.pv, 1);
         mbar_init(&bar.q_full, S::SOFTMAX);
+        mbar_init(&bar.last_v, 1);
         mbar_init(&bar.fin, 1);
         bar.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -234,7 +245,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
         for (int seq = 0; seq < 2 * tiles; ++seq) {
             seq_tile(two_q, seq, tiles, t, is_v);
             const int slot = seq % NB, j0 = u.lo + t * BN;
-            unsigned long long *full = KV8 ? &bar.raw_full[slot % 4] : &bar.full[slot];
+            unsigned long long *full = KV8 ? &bar.raw_full[slot % 4] : is_v && t == tiles - 1 ? &bar.last_v : &bar.full[slot];
             unsigned long long *empty = KV8 ? &bar.raw_empty[slot % 4] : &bar.empty[slot];
             if (seq >= NB && !wait_for(empty, ((seq / NB) - 1) & 1, abort)) break;
             if (lane == 0) mbar_arrive_expect_tx(full, KV8 ? S::RAW : TILE);
@@ -253,70 +264,74 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
         }
         if (*abort)  // what was copied has to land before the CTA leaves
             for (int seq = max(0, issued - NB); seq < issued; ++seq)
-                mbar_drain(KV8 ? &bar.raw_full[seq % NB % 4] : &bar.full[seq % NB], (seq / NB) & 1);
+            {
+                seq_tile(two_q, seq, tiles, t, is_v);
+                if (!KV8 && is_v && t == tiles - 1) mbar_drain(&bar.last_v, 0);
+                else mbar_drain(KV8 ? &bar.raw_full[seq % NB % 4] : &bar.full[seq % NB], (seq / NB) & 1);
+            }
     } else if (warp == W_MMA) {
         if (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        // ---- products
+        // ---- products, all by one thread
         constexpr uint32_t type = MB ? (1u << 7) | (1u << 10) : 0u;
         constexpr uint32_t id_s = umma_idesc(128, BN, 0, 0) | type, id_o = umma_idesc(128, D, 0, 1) | type;
-        bool ok = steps == 0 || wait_for(&bar.q_full, 0, abort);
-        tc_fence_after();
-        auto scores = [&](int j) {
-            const int t = two_q ? j >> 1 : j, seq = seq_k(two_q, t), slot = seq % SLOTS;
-            if (!wait_for(&bar.full[slot], (seq / SLOTS) & 1, abort)) return false;
+        if (steps > 0 && elect_one()) {
+            bool ok = wait_one(&bar.q_full, 0, abort);
             tc_fence_after();
-            if (lane == 0) {
-                const uint32_t qa = smem_addr(smem) + (two_q ? (j & 1) * S::QTILE : 0), ka = smem_addr(ring) + slot * TILE;
+            // (a descriptor's address field is in 16-byte units)
+            const uint64_t q_desc = desc_kmajor(smem_addr(smem)), k_desc = desc_kmajor(smem_addr(ring)),
+                           v_desc = desc_mnmajor(smem_addr(ring), BN * 128);
+            auto scores = [&](int j) {
+                const int t = two_q ? j >> 1 : j, seq = seq_k(two_q, t), slot = seq % SLOTS;
+                if (!wait_one(&bar.full[slot], (seq / SLOTS) & 1, abort)) return false;
+                tc_fence_after();
+                const uint64_t qd = q_desc + (two_q ? (j & 1) * (S::QTILE / 16) : 0), kd = k_desc + slot * (TILE / 16);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    umma_f16(tm + (j & 1) * BN, desc_kmajor(qa + (k / 4) * 128 * 128 + (k % 4) * 32),
-                             desc_kmajor(ka + (k / 4) * BN * 128 + (k % 4) * 32), id_s, k > 0);
-                if (!two_q || (j & 1)) umma_commit(&bar.empty[slot]);
+                    umma_f16(tm + (j & 1) * BN, qd + (k / 4) * (128 * 128 / 16) + (k % 4) * 2, kd + (k / 4) * (BN * 128 / 16) + (k % 4) * 2, id_s, k > 0);
                 umma_commit(&bar.s_full[j & 1]);
+                if (!two_q || (j & 1)) umma_commit(&bar.empty[slot]);
+                return true;
+            };
+            auto outputs = [&](int j) {
+                const int t = two_q ? j >> 1 : j, seq = seq_v(two_q, t, tiles), slot = seq % SLOTS;
+                if (!wait_one(&bar.full[slot], (seq / SLOTS) & 1, abort)) return false;
+                if (!wait_one(&bar.p_full[j & 1], (j >> 1) & 1, abort)) return false;
+                tc_fence_after();
+                const uint64_t vd = v_desc + slot * (TILE / 16);
+                const uint32_t o = tm + 256 + (NS == 2 ? (j & 1) * 128 : 0);
+#pragma unroll
+                for (int k = 0; k < BN / 16; ++k) umma_ts(o, tm + (j & 1) * BN + 8 * k, vd + k * (2048 / 16), id_o, k > 0 || j >= NS);
+                if (D != 128) umma_commit(&bar.pv);
+                if (!two_q || (j & 1)) umma_commit(&bar.empty[slot]);
+                // S(j + 2) overwrites P(j): products of one shape follow each other in order, of two shapes
+                // (D other than 128) the overwriting one is issued after the reading one is complete
+                return !(D != 128 && j + 2 < steps) || wait_one(&bar.pv, j & 1, abort);
+            };
+            ok = ok && scores(0);
+            if (ok && steps > 1) ok = scores(1);
+            for (int j = 0; ok && j < steps; ++j) {
+                ok = outputs(j);
+                if (ok && j + 2 < steps) ok = scores(j + 2);
             }
-            __syncwarp();
-            return true;
-        };
-        auto outputs = [&](int j) {
-            const int t = two_q ? j >> 1 : j, seq = seq_v(two_q, t, tiles), slot = seq % SLOTS;
-            if (!wait_for(&bar.full[slot], (seq / SLOTS) & 1, abort)) return false;
-            const int live = u.hi - (u.lo + t * BN);
-            if (!KV8 && live < BN && (!two_q || !(j & 1))) {
-                // values past the range
+            umma_commit(&bar.fin);
+            if (!ok) mbar_drain(&bar.fin, 0);
+        }
+        __syncwarp();
+    } else if (warp >= W_TMA && warp < W_TMA + 4) {
+        if (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (!KV8 && warp == W_TMA + 2 && tiles > 0) {
+            // ---- the last tile's values past the range; its copy lands on a barrier of its own
+            const int slot = seq_v(two_q, tiles - 1, tiles) % SLOTS, live = u.hi - (u.lo + (tiles - 1) * BN);
+            if (wait_for(&bar.last_v, 0, abort)) {
                 for (int i = lane; i < (BN - live) * 8 * S::HALVES; i += 32) {
                     const int r = live + i / (8 * S::HALVES), c = i % (8 * S::HALVES);
                     *reinterpret_cast<uint4 *>(ring + slot * TILE + (c / 8) * BN * 128 + r * 128 + (c % 8) * 16) = make_uint4(0, 0, 0, 0);
                 }
                 fence_proxy_async();
                 __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.full[slot]);
             }
-            if (!wait_for(&bar.p_full[j & 1], (j >> 1) & 1, abort)) return false;
-            tc_fence_after();
-            if (lane == 0) {
-                const uint32_t va = smem_addr(ring) + slot * TILE, o = tm + 256 + (NS == 2 ? (j & 1) * 128 : 0);
-#pragma unroll
-                for (int k = 0; k < BN / 16; ++k)
-                    umma_ts(o, tm + (j & 1) * BN + 8 * k, desc_mnmajor(va + k * 2048, BN * 128), id_o, k > 0 || j >= NS);
-                if (!two_q || (j & 1)) umma_commit(&bar.empty[slot]);
-                if (D != 128) umma_commit(&bar.pv);
-            }
-            __syncwarp();
-            // S(j + 2) overwrites P(j): products of one shape follow each other in order, of two shapes
-            // (D other than 128) the overwriting one is issued after the reading one is complete
-            if (D != 128 && j + 2 < steps && !wait_for(&bar.pv, j & 1, abort)) return false;
-            return true;
-        };
-        if (ok && steps > 0) ok = scores(0);
-        if (ok && steps > 1) ok = scores(1);
-        for (int j = 0; ok && j < steps; ++j) {
-            ok = outputs(j);
-            if (ok && j + 2 < steps) ok = scores(j + 2);
         }
-        if (steps > 0 && lane == 0) umma_commit(&bar.fin);
-        __syncwarp();
-        if (!ok) mbar_drain(&bar.fin, 0);
-    } else if (warp >= W_TMA && warp < W_TMA + 4) {
-        if (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     } else if (KV8 && warp >= W_TMA + 4) {
         if (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         // ---- 8-bit tiles to fp16
@@ -391,24 +406,33 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
         }
         const int s = warp / 4, row = tid % 128;
         // q to shared memory, K-major with the 128-byte swizzle; rows that are not there are zeros
+        const unsigned short *q16 = static_cast<const unsigned short *>(a.q) + (size_t)u.h * a.G * D;
         if (!KV8) {
-            for (int x = tid; x < (two_q ? 256 : 128) * (D / 8); x += S::SOFTMAX) {
-                const int r = x / (D / 8), c = x % (D / 8);
-                uint4 w = make_uint4(0, 0, 0, 0);
-                if (r < rows) {
-                    const long long rr = (long long)u.t * S::M + r;
-                    w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(a.q) + (u.s + rr / a.G) * a.q_stride +
-                                                              (u.h * a.G + rr % a.G) * D) + c);
+            constexpr int CH = D / 8, BATCH = 8;  // chunks of a row, loads in flight
+            const int all = (two_q ? 256 : 128) * CH;
+            for (int x0 = tid; x0 < all; x0 += BATCH * S::SOFTMAX) {
+                uint4 w[BATCH];
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) {
+                    const int x = x0 + i * S::SOFTMAX, r = x / CH, tok = (row0 + r) / a.G;
+                    w[i] = make_uint4(0, 0, 0, 0);
+                    if (r < rows)
+                        w[i] = __ldg(reinterpret_cast<const uint4 *>(q16 + (u.s + tok) * a.q_stride + (row0 + r - tok * a.G) * D) + x % CH);
                 }
-                *reinterpret_cast<uint4 *>(smem + (r / 128) * S::QTILE + (c / 8) * 128 * 128 + (r % 128) * 128 + (((c % 8) ^ (r & 7)) << 4)) = w;
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) {
+                    const int x = x0 + i * S::SOFTMAX, r = x / CH, c = x % CH;
+                    if (x < all)
+                        *reinterpret_cast<uint4 *>(smem + (r / 128) * S::QTILE + (c / 8) * 128 * 128 + (r % 128) * 128 + (((c % 8) ^ (r & 7)) << 4)) = w[i];
+                }
             }
         } else if (two_q || tid < 128) {
             // fp16 by a power of two for each row, as in dn_attn.cu
             const bool live = tid < rows;
-            const long long rr = (long long)u.t * S::M + tid;
-            const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const unsigned short *>(a.q) + (live ? (u.s + rr / a.G) * a.q_stride +
-                                                               (u.h * a.G + rr % a.G) * D : 0));
+            const int tok = (row0 + tid) / a.G;
+            const uint4 *src = reinterpret_cast<const uint4 *>(q16 + (live ? (u.s + tok) * a.q_stride + (row0 + tid - tok * a.G) * D : 0));
             float big = 0.f;
+#pragma unroll 8
             for (int c = 0; c < D / 8; ++c) {
                 const uint4 w = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
                 const unsigned v[4] = {w.x, w.y, w.z, w.w};
@@ -421,6 +445,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             const int e2 = min(max((int)(__float_as_uint(big) >> 23) - 127, -126), 126);
             const float f2 = __int_as_float((127 - e2) << 23);
             row_factor[tid] = a.scale_log2 * __int_as_float((127 + e2) << 23);
+#pragma unroll 8
             for (int c = 0; c < D / 8; ++c) {
                 const uint4 w = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
                 unsigned v[4] = {w.x, w.y, w.z, w.w};
@@ -438,12 +463,10 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
         if (KV8) bar_sync(1, S::SOFTMAX);  // row_factor
         const int r_unit = two_q ? s * 128 + row : row;  // this thread's row of the unit
         const float factor = KV8 ? row_factor[r_unit] : a.scale_log2;
-        const long long r_all = (long long)u.t * S::M + r_unit;
-        const int pos = u.first + (int)(r_all / a.G);
+        const int tok = (row0 + r_unit) / a.G, pos = u.first + tok;
         // positions of the first and last row of the stream, for whole tiles without a mask
-        const int r_first = two_q ? s * 128 : 0;
-        const int pos_first = u.first + (int)(((long long)u.t * S::M + r_first) / a.G);
-        const int pos_last = u.first + (int)(((long long)u.t * S::M + r_first + 127) / a.G);
+        const int r_first = row0 + (two_q ? s * 128 : 0);
+        const int pos_first = u.first + r_first / a.G, pos_last = u.first + (r_first + 127) / a.G;
         const uint32_t lanes = (uint32_t)(32 * (warp % 4)) << 16;
         const uint32_t o_addr = tm + lanes + 256 + (NS == 2 ? s * 128 : 0);
         float m = -INFINITY, l = 0.f;
@@ -585,9 +608,13 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                 f0 *= inv;
                 f1 *= inv;
             }
-            const long long at = (u.s + r_all / a.G) * ((long long)a.p.heads * a.G) + u.h * a.G + r_all % a.G;
+            // row of out and lse; a slot's rows are dense
+            const int at = (u.s + tok) * (a.p.heads * a.G) + u.h * a.G + (row0 + r_unit - tok * a.G);
             float *part = a.part + (size_t)(u.slot + u.c) * S::M * (D + 2);
             const bool bf = KV8 ? io_bf : BF;
+            // A warp's 32 rows x 32 columns pass through shared memory (the q tiles' place), so that eight lanes
+            // write a row's neighbouring columns; a lane writing its own row would touch 32 lines a store.
+            float *stage = reinterpret_cast<float *>(smem) + warp * (32 * 36);
 #pragma unroll 1
             for (int d = 0; d < D; d += 32) {
                 uint32_t y[1][32];
@@ -608,21 +635,23 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                         z[e + 3] = fmaf(f1, w.w, z[e + 3]);
                     }
                 }
-                if (live && final) {
-                    unsigned short *dst = static_cast<unsigned short *>(a.out) + at * D + d;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint4 w;
-                        w.x = bf ? pack2<true>(z[e], z[e + 1]) : pack2<false>(z[e], z[e + 1]);
-                        w.y = bf ? pack2<true>(z[e + 2], z[e + 3]) : pack2<false>(z[e + 2], z[e + 3]);
-                        w.z = bf ? pack2<true>(z[e + 4], z[e + 5]) : pack2<false>(z[e + 4], z[e + 5]);
-                        w.w = bf ? pack2<true>(z[e + 6], z[e + 7]) : pack2<false>(z[e + 6], z[e + 7]);
-                        *reinterpret_cast<uint4 *>(dst + e) = w;
+                for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4 *>(stage + lane * 36 + e) = make_float4(z[e], z[e + 1], z[e + 2], z[e + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = 4 * i + lane / 8, e = 4 * (lane % 8), ru = r_unit - lane + r;
+                    const int row_at = __shfl_sync(0xffffffffu, at, r);
+                    const float4 w = *reinterpret_cast<const float4 *>(stage + r * 36 + e);
+                    if (ru >= rows) continue;
+                    if (final) {
+                        uint2 h;
+                        h.x = bf ? pack2<true>(w.x, w.y) : pack2<false>(w.x, w.y);
+                        h.y = bf ? pack2<true>(w.z, w.w) : pack2<false>(w.z, w.w);
+                        *reinterpret_cast<uint2 *>(static_cast<unsigned short *>(a.out) + (size_t)row_at * D + d + e) = h;
+                    } else {
+                        *reinterpret_cast<float4 *>(part + (size_t)ru * D + d + e) = w;
                     }
-                } else if (live) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<float4 *>(part + (size_t)r_unit * D + d + e) = make_float4(z[e], z[e + 1], z[e + 2], z[e + 3]);
                 }
                 __syncwarp();
             }
