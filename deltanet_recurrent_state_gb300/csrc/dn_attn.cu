@@ -531,7 +531,8 @@ struct AttnPlan {
 AttnPlan attn_plan(int B, int total, int G, int D) {
     // rows of a request, on average over the batch
     const long long rows = B > 0 ? ((long long)total * G + B - 1) / B : 0;
-    if (rows > (D == 256 ? 16 : 32)) return {true, D == 256 ? 128 : 256, kAttnSms, D == 256 ? 64 : 128, 512};
+    if (rows > (D == 256 ? 16 : 32) && G <= 128)
+        return {true, 128 / G * G * (D == 256 ? 1 : 2), kAttnSms, D == 256 ? 64 : 128, 512};
     return {false, rows <= 16 ? 16 : 32, 4 * kAttnSms, 64, 256};
 }
 

@@ -17,13 +17,18 @@
 // descriptors read; each lane of the producer warp looks up and copies a box of its own. A page that a
 // request does not have is an out-of-range coordinate, which the copy fills with zeros. Rows of the last
 // page past the range may hold anything: their scores are masked, and their values are zeroed in
-// shared memory before the product (0 x NaN is not 0). For an 8-bit cache the boxes land in a ring of
-// raw tiles, and a warpgroup turns them into fp16 tiles (exact; the exponents go to the scores
-// and probabilities as in dn_attn.cu, with 2^7 in the place of 2^15, see below).
+// shared memory before the product (0 x NaN is not 0). q comes the same way, G heads by 128 / G tokens a
+// box, so a tile is as many whole tokens as 128 rows hold.
+//
+// 8-bit caches. The boxes land in a ring of raw tiles, and a warpgroup turns them into fp16 tiles, multiplied
+// by the powers of two 2^(E - R) <= 1 of the tokens: R is the tile's largest exponent for the keys, whose
+// 2^R joins the score's factor, and the largest so far for the values, so that tiles add up. Both products
+// are exact until an element falls below fp16's 2^-24, which is 2^-33 of the largest element. bf16 q is
+// brought to fp16 by a power of two for each row, as in dn_attn.cu.
 //
 // Running maximum. O is rescaled only when a row's maximum grows by more than 2^8: until then its
-// probabilities are at most 2^8, exact in 16 bits as before, and the division by the sum at the end
-// takes the factor out again. With the 2^7 of an 8-bit cache's values they stay below fp16's 2^16.
+// probabilities are at most 2^8, rounded to 16 bits with the same relative step, and the division by the
+// sum at the end takes the factor out again.
 //
 // Every wait is bounded in time; a wait that runs out raises the CTA's abort flag, and every role
 // leaves after its own copies and products have landed.
@@ -134,7 +139,6 @@ struct TileShape {
     static constexpr int NS = D <= 128 ? 2 : 1;      // streams
     static constexpr int BN = D <= 128 ? 128 : 64;   // tokens of a key tile
     static constexpr int HALVES = D / 64;            // 64-column boxes of a tile
-    static constexpr int M = 128 * NS;               // rows of a unit
     static constexpr int TILE = BN * D * 2;          // bytes of a 16-bit K or V tile
     static constexpr int QTILE = 128 * D * 2;
     static constexpr int SLOTS = KV8 ? (D == 64 ? 4 : 3) : (D == 64 ? 8 : 5);
@@ -144,20 +148,19 @@ struct TileShape {
     static constexpr int THREADS = SOFTMAX + 128 + (KV8 ? 128 : 0);
     static constexpr int OFF_RING = NS * QTILE;
     static constexpr int OFF_RAW = OFF_RING + SLOTS * TILE;
-    static constexpr int OFF_SCALE = OFF_RAW + RAWS * RAW;                    // [4][2][BN] floats (8 bits)
-    static constexpr int OFF_ROW = OFF_SCALE + (KV8 ? 4 * 2 * BN * 4 : 0);    // [M] row factors
-    static constexpr int OFF_BAR = OFF_ROW + M * 4;
-    static constexpr int BYTES = OFF_BAR + 512 + 1024;                        // and the alignment of the base
+    static constexpr int OFF_BAR = OFF_RAW + RAWS * RAW;
+    static constexpr int BYTES = OFF_BAR + 1024 + 1024;                        // and the alignment of the base
     static_assert(BYTES <= 232448, "shared memory of one CTA");
     static_assert(NS == 1 || 128 * (D + 4) * 4 + 1024 <= SLOTS * TILE, "the streams merge in the ring");
 };
 
 struct Bars {
-    unsigned long long full[8], empty[8], raw_full[4], raw_empty[4], scale_full[4], s_full[2], p_full[2], pv, q_full, last_v, fin;
+    unsigned long long full[8], empty[8], raw_full[4], raw_empty[4], ref_full[4], s_full[2], p_full[2], pv, q_full, q_ready, last_v, fin;
     uint32_t tmem;
-    int abort, ref[4];
+    int abort, k_ref[4], v_ref[4];
+    signed char q_exp[256];  // powers of two of bf16 q rows brought to fp16
 };
-static_assert(sizeof(Bars) <= 512, "barriers");
+static_assert(sizeof(Bars) <= 1024, "barriers");
 
 // Place of K (or V) tile t of n in the ring's order, and the other way round.
 __device__ __forceinline__ int seq_k(bool two_q, int t) { return two_q ? 2 * t : (t == 0 ? 0 : 2 * t - 1); }
@@ -174,30 +177,17 @@ __device__ __forceinline__ void seq_tile(bool two_q, int seq, int n, int &t, boo
 
 template <int D, bool BF, bool KV8>
 __global__ void __launch_bounds__(TileShape<D, KV8>::THREADS, 1)
-attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap mk,
-                 const __grid_constant__ CUtensorMap mv, bool io_bf) {
+attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap mq,
+                 const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, bool io_bf) {
     using S = TileShape<D, KV8>;
     constexpr int BN = S::BN, NS = S::NS, SLOTS = S::SLOTS, TILE = S::TILE;
     constexpr bool MB = BF && !KV8;
+    constexpr int W_TMA = S::SOFTMAX / 32, W_MMA = W_TMA + 1;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     unsigned char *ring = smem + S::OFF_RING, *raw = smem + S::OFF_RAW;
-    float *scales = reinterpret_cast<float *>(smem + S::OFF_SCALE);
-    float *row_factor = reinterpret_cast<float *>(smem + S::OFF_ROW);
     Bars &bar = *reinterpret_cast<Bars *>(smem + S::OFF_BAR);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-    grid_dep_wait();
-    grid_dep_trigger();
-    AttnUnit u;
-    if (!attn_unit<false>(a, blockIdx.x, u)) return;
-    if (u.c >= u.ranges) return;
-    const int row0 = u.t * S::M, rows = min(S::M, u.n * a.G - row0);  // (the host bounds total * heads)
-    const bool two_q = NS == 2 && rows > 128;
-    const int tiles = (u.hi - u.lo + BN - 1) / BN;
-    const int steps = two_q ? 2 * tiles : tiles;
-    constexpr int W_TMA = S::SOFTMAX / 32, W_MMA = W_TMA + 1;
-
-    if (warp == W_MMA) tmem_alloc<512>(&bar.tmem);
     if (tid == 0) {
         for (int i = 0; i < SLOTS; ++i) {
             mbar_init(&bar.full[i], KV8 ? 128 : 1);
@@ -207,19 +197,32 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             mbar_init(&bar.raw_full[i], 1);
             mbar_init(&bar.raw_empty[i], 128);
         }
-        for (int i = 0; i < 4; ++i) mbar_init(&bar.scale_full[i], 128);
+        for (int i = 0; i < 4; ++i) mbar_init(&bar.ref_full[i], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.s_full[i], 1);
             mbar_init(&bar.p_full[i], 128);
         }
         mbar_init(&bar.pv, 1);
-        mbar_init(&bar.q_full, S::SOFTMAX);
+        mbar_init(&bar.q_full, 1);
+        mbar_init(&bar.q_ready, S::SOFTMAX);
         mbar_init(&bar.last_v, 1);
         mbar_init(&bar.fin, 1);
         bar.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async();
     }
+    grid_dep_wait();
+    grid_dep_trigger();
+    AttnUnit u;
+    if (!attn_unit<false>(a, blockIdx.x, u)) return;
+    if (u.c >= u.ranges) return;
+    const int mq_rows = a.M / NS;                                 // rows of a q tile: whole tokens, at most 128
+    const int row0 = u.t * a.M, rows = min(a.M, u.n * a.G - row0);  // (the host bounds total * heads)
+    const bool two_q = NS == 2 && rows > mq_rows;
+    const int tiles = (u.hi - u.lo + BN - 1) / BN;
+    const int steps = two_q ? 2 * tiles : tiles;
+
+    if (warp == W_MMA) tmem_alloc<512>(&bar.tmem);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -233,6 +236,14 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
         const int boxes = BN / R * H2, sub = lane / H2, half = lane % H2;
         constexpr int NB = KV8 ? S::RAWS : SLOTS;
         int issued = 0;
+        if (tiles > 0 && lane == 0) {
+            const int tokens = 128 / a.G, boxes_q = S::HALVES * (two_q ? 2 : 1);
+            mbar_arrive_expect_tx(&bar.q_full, boxes_q * mq_rows * 128);
+            for (int i = 0; i < boxes_q; ++i)
+                tma_load_3d(smem + i / S::HALVES * S::QTILE + i % S::HALVES * (128 * 128), &mq, i % S::HALVES * 64, u.h * a.G,
+                            u.s + row0 / a.G + i / S::HALVES * tokens, &bar.q_full);
+        }
+        __syncwarp();
         auto look = [&](int t) {
             const int j = u.lo + t * BN + sub * R;
             const int pg = lane < boxes && j < u.hi ? pool_page(a.p, u.b, j) : -1;
@@ -262,20 +273,22 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                 pg = look(t2);
             }
         }
-        if (*abort)  // what was copied has to land before the CTA leaves
+        if (*abort) {  // what was copied has to land before the CTA leaves
+            if (tiles > 0) mbar_drain(&bar.q_full, 0);
             for (int seq = max(0, issued - NB); seq < issued; ++seq)
             {
                 seq_tile(two_q, seq, tiles, t, is_v);
                 if (!KV8 && is_v && t == tiles - 1) mbar_drain(&bar.last_v, 0);
                 else mbar_drain(KV8 ? &bar.raw_full[seq % NB % 4] : &bar.full[seq % NB], (seq / NB) & 1);
             }
+        }
     } else if (warp == W_MMA) {
         if (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         // ---- products, all by one thread
         constexpr uint32_t type = MB ? (1u << 7) | (1u << 10) : 0u;
         constexpr uint32_t id_s = umma_idesc(128, BN, 0, 0) | type, id_o = umma_idesc(128, D, 0, 1) | type;
         if (steps > 0 && elect_one()) {
-            bool ok = wait_one(&bar.q_full, 0, abort);
+            bool ok = wait_one(&bar.q_full, 0, abort) && (!(KV8 && io_bf) || wait_one(&bar.q_ready, 0, abort));
             tc_fence_after();
             // (a descriptor's address field is in 16-byte units)
             const uint64_t q_desc = desc_kmajor(smem_addr(smem)), k_desc = desc_kmajor(smem_addr(ring)),
@@ -336,7 +349,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
         if (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         // ---- 8-bit tiles to fp16
         const int c = tid - (W_TMA + 4) * 32;
-        int ref = 0;
+        int ref[2] = {0, 0}, ref_most = 0;  // the values' R of the last two tiles
         for (int seq = 0; seq < 2 * tiles; ++seq) {
             int t;
             bool is_v;
@@ -344,12 +357,12 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             const int j0 = u.lo + t * BN, live = min(BN, u.hi - j0);
             // exponents of tokens 4 lane .. + 3, by every warp for itself (in the shadow of the waits)
             unsigned ek = 0, ev = 0;
-            if (!is_v && 4 * lane < live) {
+            if (4 * lane < live) {
                 const int pg = pool_page(a.p, u.b, j0 + 4 * lane);
                 if (pg >= 0) {
                     const long long at = ((((long long)pg * a.p.heads + u.h)) << a.p.page_shift) + ((j0 + 4 * lane) & ((1 << a.p.page_shift) - 1));
-                    ek = __ldg(reinterpret_cast<const unsigned *>(a.ke + at));
                     ev = __ldg(reinterpret_cast<const unsigned *>(a.ve + at));
+                    if (!is_v) ek = __ldg(reinterpret_cast<const unsigned *>(a.ke + at));
                     if (live - 4 * lane < 4) {  // bytes past the range are not the request's
                         const unsigned mask = (1u << (8 * (live - 4 * lane))) - 1u;
                         ek &= mask;
@@ -360,35 +373,42 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             const int slot = seq % SLOTS, rs = seq % (KV8 ? S::RAWS : 1);
             if (seq >= SLOTS && !wait_for(&bar.empty[slot], ((seq / SLOTS) - 1) & 1, abort)) break;
             if (!wait_for(&bar.raw_full[rs], (seq / (KV8 ? S::RAWS : 1)) & 1, abort)) break;
-            if (!is_v) {
-                // factors of the tile's scores and probabilities; the largest value exponent so far
-                unsigned top = __vmaxu4(ev, ev >> 16);
-                top = __reduce_max_sync(0xffffffffu, max(top & 0xffu, (top >> 8) & 0xffu));
-                ref = max(ref, (int)top);
-                if (lane / 8 == warp % 4 && 4 * lane < BN) {  // each warp writes 32 tokens
-                    float *kf = scales + (t & 3) * 2 * BN + 4 * lane;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        kf[e] = exp_byte((ek >> (8 * e)) & 0xffu);
-                        const int x = (int)((ev >> (8 * e)) & 0xffu) - ref + 7 + 127;
-                        kf[BN + e] = 4 * lane + e < live ? __int_as_float(max(x, 0) << 23) : 0.f;
-                    }
+            auto largest = [](unsigned e) {
+                const unsigned m = __vmaxu4(e, e >> 16);
+                return (int)__reduce_max_sync(0xffffffffu, max(m & 0xffu, (m >> 8) & 0xffu));
+            };
+            int R;
+            if (!is_v) {  // with the keys, the softmax learns both
+                R = largest(ek);
+                ref_most = max(ref_most, largest(ev));
+                (t & 1 ? ref[1] : ref[0]) = ref_most;
+                if (c == 0) {
+                    bar.k_ref[t & 3] = R;
+                    bar.v_ref[t & 3] = ref_most;
+                    mbar_arrive(&bar.ref_full[t & 3]);
                 }
-                if (c == 0) bar.ref[t & 3] = ref;
-                mbar_arrive(&bar.scale_full[t & 3]);
+            } else {
+                R = t & 1 ? ref[1] : ref[0];
             }
+            const unsigned e4 = is_v ? ev : ek;
             const unsigned char *src = raw + rs * S::RAW;
             unsigned char *dst = ring + slot * TILE;
 #pragma unroll 4
             for (int i = 0; i < BN * D / 16 / 128; ++i) {
                 const int x = i * 128 + c, r = x / (D / 16), e = x % (D / 16) * 16, half = e / 64, ch = e % 64 / 8;
+                // 2^(E - R) in fp16: subnormal below 2^-14, zero below 2^-24; rows past the range are zeros
+                const int E = (int)((__shfl_sync(0xffffffffu, e4, r / 4) >> (8 * (r & 3))) & 0xffu) - R;
+                const __half2 f = __float2half2_rn(__int_as_float(max(E + 127, 0) << 23));
                 uint4 w = *reinterpret_cast<const uint4 *>(src + x * 16);
                 if (r >= live) w = make_uint4(0, 0, 0, 0);
+                auto two = [&](unsigned v) {
+                    const unsigned h = unpack_e4m3((unsigned short)v);
+                    const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&h), f);
+                    return *reinterpret_cast<const unsigned *>(&y);
+                };
                 uint4 o[2];
-                o[0] = make_uint4(unpack_e4m3((unsigned short)w.x), unpack_e4m3((unsigned short)(w.x >> 16)),
-                                  unpack_e4m3((unsigned short)w.y), unpack_e4m3((unsigned short)(w.y >> 16)));
-                o[1] = make_uint4(unpack_e4m3((unsigned short)w.z), unpack_e4m3((unsigned short)(w.z >> 16)),
-                                  unpack_e4m3((unsigned short)w.w), unpack_e4m3((unsigned short)(w.w >> 16)));
+                o[0] = make_uint4(two(w.x), two(w.x >> 16), two(w.y), two(w.y >> 16));
+                o[1] = make_uint4(two(w.z), two(w.z >> 16), two(w.w), two(w.w >> 16));
                 unsigned char *row = dst + half * BN * 128 + r * 128;
                 const int first = half & 1;  // lanes of neighbouring halves store to different banks
                 *reinterpret_cast<uint4 *>(row + (((ch + first) ^ (r & 7)) << 4)) = first ? o[1] : o[0];
@@ -405,74 +425,54 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         }
         const int s = warp / 4, row = tid % 128;
-        // q to shared memory, K-major with the 128-byte swizzle; rows that are not there are zeros
-        const unsigned short *q16 = static_cast<const unsigned short *>(a.q) + (size_t)u.h * a.G * D;
-        if (!KV8) {
-            constexpr int CH = D / 8, BATCH = 8;  // chunks of a row, loads in flight
-            const int all = (two_q ? 256 : 128) * CH;
-            for (int x0 = tid; x0 < all; x0 += BATCH * S::SOFTMAX) {
-                uint4 w[BATCH];
-#pragma unroll
-                for (int i = 0; i < BATCH; ++i) {
-                    const int x = x0 + i * S::SOFTMAX, r = x / CH, tok = (row0 + r) / a.G;
-                    w[i] = make_uint4(0, 0, 0, 0);
-                    if (r < rows)
-                        w[i] = __ldg(reinterpret_cast<const uint4 *>(q16 + (u.s + tok) * a.q_stride + (row0 + r - tok * a.G) * D) + x % CH);
-                }
-#pragma unroll
-                for (int i = 0; i < BATCH; ++i) {
-                    const int x = x0 + i * S::SOFTMAX, r = x / CH, c = x % CH;
-                    if (x < all)
-                        *reinterpret_cast<uint4 *>(smem + (r / 128) * S::QTILE + (c / 8) * 128 * 128 + (r % 128) * 128 + (((c % 8) ^ (r & 7)) << 4)) = w[i];
-                }
-            }
-        } else if (two_q || tid < 128) {
-            // fp16 by a power of two for each row, as in dn_attn.cu
-            const bool live = tid < rows;
-            const int tok = (row0 + tid) / a.G;
-            const uint4 *src = reinterpret_cast<const uint4 *>(q16 + (live ? (u.s + tok) * a.q_stride + (row0 + tid - tok * a.G) * D : 0));
-            float big = 0.f;
-#pragma unroll 8
-            for (int c = 0; c < D / 8; ++c) {
-                const uint4 w = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-                const unsigned v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 f = io_bf ? unpack2<true>(v[e]) : unpack2<false>(v[e]);
-                    big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
-                }
-            }
-            const int e2 = min(max((int)(__float_as_uint(big) >> 23) - 127, -126), 126);
-            const float f2 = __int_as_float((127 - e2) << 23);
-            row_factor[tid] = a.scale_log2 * __int_as_float((127 + e2) << 23);
-#pragma unroll 8
-            for (int c = 0; c < D / 8; ++c) {
-                const uint4 w = live ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-                unsigned v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float2 f = io_bf ? unpack2<true>(v[e]) : unpack2<false>(v[e]);
-                    v[e] = pack2<false>(f.x * f2, f.y * f2);
-                }
-                *reinterpret_cast<uint4 *>(smem + (tid / 128) * S::QTILE + (c / 8) * 128 * 128 + row * 128 + (((c % 8) ^ (row & 7)) << 4)) =
-                    make_uint4(v[0], v[1], v[2], v[3]);
-            }
-        }
-        fence_proxy_async();
-        mbar_arrive(&bar.q_full);
-        if (KV8) bar_sync(1, S::SOFTMAX);  // row_factor
-        const int r_unit = two_q ? s * 128 + row : row;  // this thread's row of the unit
-        const float factor = KV8 ? row_factor[r_unit] : a.scale_log2;
+        const int r_unit = two_q ? s * mq_rows + row : row;  // this thread's row of the unit
         const int tok = (row0 + r_unit) / a.G, pos = u.first + tok;
         // positions of the first and last row of the stream, for whole tiles without a mask
-        const int r_first = row0 + (two_q ? s * 128 : 0);
-        const int pos_first = u.first + r_first / a.G, pos_last = u.first + (r_first + 127) / a.G;
+        const int tok_first = (row0 + (two_q ? s * mq_rows : 0)) / a.G, pos_first = u.first + tok_first, pos_last = pos_first + 128 / a.G - 1;
+        float q_factor = a.scale_log2;
+        bool ok = true, any = false;
+        if (KV8 && io_bf && tiles > 0) {
+            // bf16 rows to fp16 by a power of two, in place (which chunk is which does not matter here)
+            ok = wait_for(&bar.q_full, 0, abort);
+            if (two_q || s == 0) {
+                unsigned char *mine = smem + (two_q ? s * S::QTILE : 0) + row * 128;
+                float big = 0.f;
+#pragma unroll 4
+                for (int x = 0; x < 8 * S::HALVES; ++x) {
+                    const uint4 w = *reinterpret_cast<const uint4 *>(mine + x / 8 * (128 * 128) + ((x + row) & 7) * 16);
+                    const unsigned v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 f = unpack2<true>(v[e]);
+                        big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
+                }
+                const int e2 = min(max((int)(__float_as_uint(big) >> 23) - 127, -126), 126);
+                const float f2 = __int_as_float((127 - e2) << 23);
+                bar.q_exp[r_unit] = (signed char)e2;
+#pragma unroll 4
+                for (int x = 0; x < 8 * S::HALVES; ++x) {
+                    uint4 *at = reinterpret_cast<uint4 *>(mine + x / 8 * (128 * 128) + ((x + row) & 7) * 16);
+                    const uint4 w = *at;
+                    unsigned v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 f = unpack2<true>(v[e]);
+                        v[e] = pack2<false>(f.x * f2, f.y * f2);
+                    }
+                    *at = make_uint4(v[0], v[1], v[2], v[3]);
+                }
+                fence_proxy_async();
+            }
+            mbar_arrive(&bar.q_ready);
+            bar_sync(1, S::SOFTMAX);
+            q_factor *= __int_as_float((127 + bar.q_exp[r_unit]) << 23);
+        }
         const uint32_t lanes = (uint32_t)(32 * (warp % 4)) << 16;
         const uint32_t o_addr = tm + lanes + 256 + (NS == 2 ? s * 128 : 0);
         float m = -INFINITY, l = 0.f;
         int ref = 0;
-        bool ok = true, any = false;
-        for (int j = NS == 2 ? s : 0; j < steps; j += NS) {
+        for (int j = NS == 2 ? s : 0; ok && j < steps; j += NS) {
             const int t = two_q ? j >> 1 : j, j0 = u.lo + t * BN;
             const uint32_t s_addr = tm + lanes + (j & 1) * BN;
             if (!wait_for(&bar.s_full[j & 1], (j >> 1) & 1, abort)) { ok = false; break; }
@@ -480,38 +480,34 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             uint32_t x[BN / 32][32];
 #pragma unroll
             for (int i = 0; i < BN / 32; ++i) tmem_ld32_start(s_addr + 32 * i, x[i]);
-            const float *kf = scales + (t & 3) * 2 * BN, *vf = kf + BN;
+            float factor = q_factor;
             int ref_now = 0;
             if (KV8) {
-                if (!wait_for(&bar.scale_full[t & 3], (t >> 2) & 1, abort)) { ok = false; break; }
-                ref_now = bar.ref[t & 3];
+                if (!wait_for(&bar.ref_full[t & 3], (t >> 2) & 1, abort)) ok = false;
+                factor *= exp_byte(bar.k_ref[t & 3]);
+                ref_now = bar.v_ref[t & 3];
             }
             tmem_wait_ld(x);
-            if (KV8) {
-#pragma unroll
-                for (int i = 0; i < BN; i += 4) {
-                    const float4 f = *reinterpret_cast<const float4 *>(kf + i);
-                    x[i / 32][i % 32] = __float_as_uint(__uint_as_float(x[i / 32][i % 32]) * f.x);
-                    x[i / 32][i % 32 + 1] = __float_as_uint(__uint_as_float(x[i / 32][i % 32 + 1]) * f.y);
-                    x[i / 32][i % 32 + 2] = __float_as_uint(__uint_as_float(x[i / 32][i % 32 + 2]) * f.z);
-                    x[i / 32][i % 32 + 3] = __float_as_uint(__uint_as_float(x[i / 32][i % 32 + 3]) * f.w);
-                }
-            }
+            if (!ok) break;
             if (j0 + BN - 1 > pos_first || j0 + BN > u.hi || (a.window && j0 <= pos_last - a.window)) {
+                // columns least < i <= most are seen, as bits of each 32
                 const int most = min(pos, u.hi - 1) - j0, least = a.window ? pos - a.window - j0 : -1;
 #pragma unroll
-                for (int i = 0; i < BN; ++i)
-                    if (i > most || i <= least) x[i / 32][i % 32] = 0xff800000u;  // -inf
-            }
-            float b0 = -INFINITY, b1 = -INFINITY, b2 = -INFINITY, b3 = -INFINITY;
+                for (int i = 0; i < BN / 32; ++i) {
+                    const int up = most - 32 * i, down = least - 32 * i;
+                    const unsigned keep = (up >= 31 ? 0xffffffffu : up < 0 ? 0u : (2u << up) - 1u) &
+                                          ~(down >= 31 ? 0xffffffffu : down < 0 ? 0u : (2u << down) - 1u);
 #pragma unroll
-            for (int i = 0; i < BN; i += 4) {
-                b0 = fmaxf(b0, __uint_as_float(x[i / 32][i % 32]));
-                b1 = fmaxf(b1, __uint_as_float(x[i / 32][i % 32 + 1]));
-                b2 = fmaxf(b2, __uint_as_float(x[i / 32][i % 32 + 2]));
-                b3 = fmaxf(b3, __uint_as_float(x[i / 32][i % 32 + 3]));
+                    for (int e = 0; e < 32; ++e) x[i][e] = keep & (1u << e) ? x[i][e] : 0xff800000u;  // -inf
+                }
             }
-            const float big = fmaxf(fmaxf(b0, b1), fmaxf(b2, b3)) * factor;
+            float b[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int i = 0; i < BN; i += 8)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    b[e] = fmaxf(fmaxf(b[e], __uint_as_float(x[i / 32][i % 32 + 2 * e])), __uint_as_float(x[i / 32][i % 32 + 2 * e + 1]));
+            const float big = fmaxf(fmaxf(b[0], b[1]), fmaxf(b[2], b[3])) * factor;
             if (!any) {
                 any = true;
                 m = big;
@@ -542,25 +538,21 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                 }
             }
             const float base = m == -INFINITY ? 0.f : m;
-            float l0 = 0.f, l1 = 0.f;
+            const float2 f2 = make_float2(factor, factor), b2 = make_float2(-base, -base);
+            float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int i = 0; i < BN / 32; ++i) {
                 uint32_t p[16];
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
-                    float p0 = ex2(fmaf(__uint_as_float(x[i][e]), factor, -base)), p1 = ex2(fmaf(__uint_as_float(x[i][e + 1]), factor, -base));
-                    l0 += p0;
-                    l1 += p1;
-                    if (KV8) {
-                        const float2 f = *reinterpret_cast<const float2 *>(vf + 32 * i + e);
-                        p0 *= f.x;
-                        p1 *= f.y;
-                    }
-                    p[e / 2] = pack2<MB>(p0, p1);
+                    float2 y = __ffma2_rn(make_float2(__uint_as_float(x[i][e]), __uint_as_float(x[i][e + 1])), f2, b2);
+                    y = make_float2(ex2(y.x), ex2(y.y));
+                    l2[(e >> 1) & 1] = __fadd2_rn(l2[(e >> 1) & 1], y);
+                    p[e / 2] = pack2<MB>(y.x, y.y);
                 }
                 tmem_st16(s_addr + 16 * i, p);
             }
-            l += l0 + l1;
+            l += (l2[0].x + l2[1].x) + (l2[0].y + l2[1].y);
             tmem_wait_st();
             tc_fence_before();
             mbar_arrive(&bar.p_full[j & 1]);
@@ -568,7 +560,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
         // ---- the outputs (tensor-memory loads are the whole warp's, stores each row's own)
         if (steps > 0 && ok) ok = wait_for(&bar.fin, 0, abort);
         tc_fence_after();
-        const float unit = KV8 ? ex2((float)(ref - 127 - 7)) : 1.f;
+        const float unit = KV8 ? ex2((float)(ref - 127)) : 1.f;
         constexpr int PITCH = D + 4;
         float *mo = reinterpret_cast<float *>(ring);
         float2 *ml = reinterpret_cast<float2 *>(ring + 128 * PITCH * 4);
@@ -590,8 +582,8 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             }
             bar_sync(2, 256);
         }
-        if (ok && !(merge && s == 1) && __any_sync(0xffffffffu, r_unit < rows)) {
-            const bool live = r_unit < rows, other = merge && tiles > 1;  // (stream 1 has a tile of its own)
+        if (ok && !(merge && s == 1) && __any_sync(0xffffffffu, row < mq_rows && r_unit < rows)) {
+            const bool other = merge && tiles > 1;  // (stream 1 has a tile of its own)
             float top = m, f0 = unit, f1 = 0.f, sum = l;
             if (other) {
                 const float2 y = ml[row];
@@ -610,7 +602,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             }
             // row of out and lse; a slot's rows are dense
             const int at = (u.s + tok) * (a.p.heads * a.G) + u.h * a.G + (row0 + r_unit - tok * a.G);
-            float *part = a.part + (size_t)(u.slot + u.c) * S::M * (D + 2);
+            float *part = a.part + (size_t)(u.slot + u.c) * a.M * (D + 2);
             const bool bf = KV8 ? io_bf : BF;
             // A warp's 32 rows x 32 columns pass through shared memory (the q tiles' place), so that eight lanes
             // write a row's neighbouring columns; a lane writing its own row would touch 32 lines a store.
@@ -641,9 +633,9 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int r = 4 * i + lane / 8, e = 4 * (lane % 8), ru = r_unit - lane + r;
-                    const int row_at = __shfl_sync(0xffffffffu, at, r);
+                    const int row_at = __shfl_sync(0xffffffffu, at, r), r_tile = row - lane + r;
                     const float4 w = *reinterpret_cast<const float4 *>(stage + r * 36 + e);
-                    if (ru >= rows) continue;
+                    if (r_tile >= mq_rows || ru >= rows) continue;
                     if (final) {
                         uint2 h;
                         h.x = bf ? pack2<true>(w.x, w.y) : pack2<false>(w.x, w.y);
@@ -655,10 +647,11 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                 }
                 __syncwarp();
             }
+            const bool live = row < mq_rows && r_unit < rows;
             if (live && final) {
                 if (a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945f;
             } else if (live) {
-                *reinterpret_cast<float2 *>(part + (size_t)S::M * D + 2 * r_unit) = make_float2(top, sum);
+                *reinterpret_cast<float2 *>(part + (size_t)a.M * D + 2 * r_unit) = make_float2(top, sum);
             }
         }
         tc_fence_before();
@@ -682,14 +675,25 @@ bool pool_map(CUtensorMap *m, const void *base, const AttnArgs &a, int D, int eb
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// q as [total][heads][D]: boxes of 64 columns, G heads and 128 / G tokens.
+bool q_map(CUtensorMap *m, const AttnArgs &a, int D) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.p.heads * a.G, (cuuint64_t)a.p.total};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)a.q_stride * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)a.G, (cuuint32_t)(128 / a.G)}, es[3] = {1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void *>(a.q), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, bool BF, bool KV8>
 dn_status launch_tile(const AttnArgs &a, bool io_bf, unsigned grid, cudaStream_t st) {
     using S = TileShape<D, KV8>;
     const int rows = 1 << a.p.page_shift < S::BN ? 1 << a.p.page_shift : S::BN;
-    CUtensorMap mk, mv;
-    if (!pool_map(&mk, a.kc, a, D, KV8 ? 1 : 2, rows) || !pool_map(&mv, a.vc, a, D, KV8 ? 1 : 2, rows)) return DN_ERR_CUDA;
+    CUtensorMap mq, mk, mv;
+    if (!q_map(&mq, a, D) || !pool_map(&mk, a.kc, a, D, KV8 ? 1 : 2, rows) || !pool_map(&mv, a.vc, a, D, KV8 ? 1 : 2, rows)) return DN_ERR_CUDA;
     cudaFuncSetAttribute(attn_tile_kernel<D, BF, KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
-    launch_pdl(attn_tile_kernel<D, BF, KV8>, dim3(grid), dim3(S::THREADS), S::BYTES, st, a, mk, mv, io_bf);
+    launch_pdl(attn_tile_kernel<D, BF, KV8>, dim3(grid), dim3(S::THREADS), S::BYTES, st, a, mq, mk, mv, io_bf);
     return DN_OK;
 }
 
