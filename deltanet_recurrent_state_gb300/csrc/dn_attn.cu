@@ -446,24 +446,23 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a, bool io_bf) {
 }
 
 // ---- join: the ranges of a tile, in their order ----------------------------------------------
-// A CTA joins 4 rows of one tile and head: two warps a row, each over half of the ranges, with a lane
-// holding D / 32 columns. The partials were written by the launch before and are in L2.
-constexpr int kJoinRows = 4;
-
-template <int D>
-__global__ void __launch_bounds__(64 * kJoinRows)
+// A CTA joins kJoinRows rows of one tile and head, its eight warps in equal groups a row: each warp adds
+// an eighth (or fewer) of the ranges, a lane holding D / 32 columns, and the warps' sums are added in order.
+// The partials were written by the launch before and are in L2; a row is few loads deep.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(256)
 attn_join_kernel(const __grid_constant__ AttnArgs a, bool bf) {
-    constexpr int E = D / 32;
-    __shared__ float sh[kJoinRows][D];
-    __shared__ float2 sml[kJoinRows];
+    constexpr int E = D / 32, WPR = 8 / ROWS;
+    __shared__ float sh[8][D];
+    __shared__ float2 sml[8];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
     grid_dep_wait();
     grid_dep_trigger();
     AttnUnit u;
     if (!attn_unit<true>(a, blockIdx.x, u) || u.ranges < 2) return;
     const int M = a.M, row0 = u.t * M, rows = min(M, u.n * a.G - row0);
-    const int r = blockIdx.y * kJoinRows + (warp >> 1), half = warp & 1;
-    if ((int)(blockIdx.y * kJoinRows) >= rows) return;
+    const int r = blockIdx.y * ROWS + warp / WPR, w = warp % WPR;
+    if ((int)(blockIdx.y * ROWS) >= rows) return;
     float acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
@@ -471,53 +470,57 @@ attn_join_kernel(const __grid_constant__ AttnArgs a, bool bf) {
     if (r < rows) {
         const size_t slot = (size_t)M * (D + 2);
         const float *p = a.part + u.slot * slot;
-        const int c0 = half ? (u.ranges + 1) / 2 : 0, c1 = half ? u.ranges : (u.ranges + 1) / 2;
-        for (int c = c0; c < c1; ++c)
-            top = fmaxf(top, __ldg(p + c * slot + M * D + 2 * r));
-        const float base = top == -INFINITY ? 0.f : top;
+        const int per = (u.ranges + WPR - 1) / WPR, c0 = w * per, c1 = min(u.ranges, c0 + per);
 #pragma unroll 4
         for (int c = c0; c < c1; ++c) {
             const float2 y = __ldg(reinterpret_cast<const float2 *>(p + c * slot + M * D + 2 * r));
-            const float f = exp2_fast(y.x - base);
-            sum = fmaf(f, y.y, sum);
             const float *v = p + c * slot + (size_t)r * D + E * lane;
             float x[E];
             if (E == 2) {
-                const float2 w = __ldg(reinterpret_cast<const float2 *>(v));
-                x[0] = w.x; x[E - 1] = w.y;
+                const float2 q = __ldg(reinterpret_cast<const float2 *>(v));
+                x[0] = q.x; x[E - 1] = q.y;
             } else {
 #pragma unroll
                 for (int e = 0; e < E; e += 4) {
-                    const float4 w = __ldg(reinterpret_cast<const float4 *>(v + e));
-                    x[e] = w.x; x[(e + 1) % E] = w.y; x[(e + 2) % E] = w.z; x[(e + 3) % E] = w.w;
+                    const float4 q = __ldg(reinterpret_cast<const float4 *>(v + e));
+                    x[e] = q.x; x[(e + 1) % E] = q.y; x[(e + 2) % E] = q.z; x[(e + 3) % E] = q.w;
                 }
             }
+            const float most = fmaxf(top, y.x), base = most == -INFINITY ? 0.f : most;
+            const float f0 = exp2_fast(top - base), f1 = exp2_fast(y.x - base);
+            top = most;
+            sum = fmaf(f1, y.y, f0 * sum);
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = fmaf(f, x[e], acc[e]);
-        }
-        if (half) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) sh[warp >> 1][E * lane + e] = acc[e];
-            if (lane == 0) sml[warp >> 1] = make_float2(top, sum);
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(f1, x[e], f0 * acc[e]);
         }
     }
+    if (w) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) sh[warp][E * lane + e] = acc[e];
+        if (lane == 0) sml[warp] = make_float2(top, sum);
+    }
     __syncthreads();
-    if (half || r >= rows) return;
-    const float2 y = sml[warp >> 1];
-    const float all = fmaxf(top, y.x), base = all == -INFINITY ? 0.f : all;
-    const float f0 = exp2_fast(top - base), f1 = exp2_fast(y.x - base);
-    sum = f0 * sum + f1 * y.y;
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
+    if (w || r >= rows) return;
+    float all = top;
+#pragma unroll
+    for (int i = 1; i < WPR; ++i) all = fmaxf(all, sml[warp + i].x);
+    const float base = all == -INFINITY ? 0.f : all, f0 = exp2_fast(top - base);
+    sum *= f0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] *= f0;
+#pragma unroll
+    for (int i = 1; i < WPR; ++i) {
+        const float f = exp2_fast(sml[warp + i].x - base);
+        sum = fmaf(f, sml[warp + i].y, sum);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(f, sh[warp + i][E * lane + e], acc[e]);
+    }
+    const float inv = sum > 0.f ? 1.f / sum : sum != sum ? sum : 0.f;  // NaN stays NaN
     const int tok = (row0 + r) / a.G;
     const size_t at = (u.s + tok) * (a.p.heads * a.G) + u.h * a.G + row0 + r - tok * a.G;
     unsigned *dst = reinterpret_cast<unsigned *>(static_cast<unsigned short *>(a.out) + at * D + E * lane);
 #pragma unroll
-    for (int e = 0; e < E; e += 2) {
-        float x0 = (f0 * acc[e] + f1 * sh[warp >> 1][E * lane + e]) * inv;
-        float x1 = (f0 * acc[e + 1] + f1 * sh[warp >> 1][E * lane + e + 1]) * inv;
-        if (sum != sum) x0 = x1 = sum;
-        dst[e / 2] = bf ? pack2<true>(x0, x1) : pack2<false>(x0, x1);
-    }
+    for (int e = 0; e < E; e += 2) dst[e / 2] = bf ? pack2<true>(acc[e] * inv, acc[e + 1] * inv) : pack2<false>(acc[e] * inv, acc[e + 1] * inv);
     if (lane == 0 && a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (all + log2f(sum)) * 0.693147180559945f;
 }
 
@@ -552,13 +555,21 @@ void launch_rows(const AttnArgs &a, bool bf, bool kv8, unsigned grid, cudaStream
 
 }  // namespace
 
+template <int ROWS>
+void launch_join(const AttnArgs &a, int D, bool bf, unsigned pairs, unsigned rows, cudaStream_t st) {
+    const dim3 grid(pairs, (rows + ROWS - 1) / ROWS);
+    if (D == 64) launch_pdl(attn_join_kernel<64, ROWS>, grid, dim3(256), 0, st, a, bf);
+    else if (D == 128) launch_pdl(attn_join_kernel<128, ROWS>, grid, dim3(256), 0, st, a, bf);
+    else launch_pdl(attn_join_kernel<256, ROWS>, grid, dim3(256), 0, st, a, bf);
+}
+
+// Few tiles have many ranges each: a CTA a row, as long as that is at most a few waves of CTAs. Many tiles
+// have few ranges, and most CTAs of a grid that covers them all have nothing to join: eight rows a CTA.
 void launch_attn_join(const AttnArgs &a, int D, bool bf, cudaStream_t st) {
     const long long pairs = min((long long)a.target, attn_tiles_bound(a.p.B, a.p.total, a.G, a.M) * a.p.heads);
     const long long rows = min((long long)a.M, (long long)a.p.total * a.G);
-    const dim3 grid((unsigned)pairs, (unsigned)((rows + kJoinRows - 1) / kJoinRows));
-    if (D == 64) launch_pdl(attn_join_kernel<64>, grid, dim3(64 * kJoinRows), 0, st, a, bf);
-    else if (D == 128) launch_pdl(attn_join_kernel<128>, grid, dim3(64 * kJoinRows), 0, st, a, bf);
-    else launch_pdl(attn_join_kernel<256>, grid, dim3(64 * kJoinRows), 0, st, a, bf);
+    if (pairs * rows <= 8 * kAttnSms) launch_join<1>(a, D, bf, (unsigned)pairs, (unsigned)rows, st);
+    else launch_join<8>(a, D, bf, (unsigned)pairs, (unsigned)rows, st);
 }
 
 }  // namespace dn

@@ -4,8 +4,9 @@
 // has an SM's tensor memory to itself: S = Q K^T of 128 rows by BN cached tokens, P = exp2(S - m),
 // O += P V, with S, P and O in tensor memory and nothing but Q, K and V in shared memory.
 //
-// Steps and streams. Step j computes S into buffer j & 1; its softmax turns that buffer into P (16 bits,
-// in the same columns); P V is added to an accumulator. The tensor core runs S(0), S(1), then P V(j),
+// Steps and streams. Step j computes S into buffer j & 1; its softmax turns that into P (16 bits, in the
+// same columns if D = 128); P V is added to an accumulator. S(j + 2) may overwrite P(j) because products of
+// one shape run in the order of their issue; for the other D the shapes differ and P has its own columns. The tensor core runs S(0), S(1), then P V(j),
 // S(j + 2), .., so one step's softmax always has another step's products beside it. For D <= 128 the
 // even and the odd steps are two streams with a warpgroup and an accumulator each: if the unit has more
 // than 128 rows (a prompt's chunk) the streams are its two halves of rows over the same keys, else
@@ -146,12 +147,15 @@ struct TileShape {
     static constexpr int RAWS = KV8 ? (D == 64 ? 4 : 3) : 0;
     static constexpr int SOFTMAX = 128 * NS;         // threads of the softmax warpgroups
     static constexpr int THREADS = SOFTMAX + 128 + (KV8 ? 128 : 0);
+    // columns of tensor memory: S at 0 and BN, P in the place of S for D = 128 (where that fills the
+    // 512 columns), else beside it
+    static constexpr int COL_P = D == 128 ? 0 : D == 64 ? 384 : 128, P_STEP = D == 128 ? BN : BN / 2, COL_O = 256, O_STEP = D;
     static constexpr int OFF_RING = NS * QTILE;
     static constexpr int OFF_RAW = OFF_RING + SLOTS * TILE;
     static constexpr int OFF_BAR = OFF_RAW + RAWS * RAW;
     static constexpr int BYTES = OFF_BAR + 1024 + 1024;                        // and the alignment of the base
     static_assert(BYTES <= 232448, "shared memory of one CTA");
-    static_assert(NS == 1 || 128 * (D + 4) * 4 + 1024 <= SLOTS * TILE, "the streams merge in the ring");
+    static_assert(NS == 1 || 8192 + 128 * (D + 4) * 4 + 1024 <= SLOTS * TILE, "the streams merge in the ring");
 };
 
 struct Bars {
@@ -244,17 +248,24 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                             u.s + row0 / a.G + i / S::HALVES * tokens, &bar.q_full);
         }
         __syncwarp();
-        auto look = [&](int t) {
-            const int j = u.lo + t * BN + sub * R;
-            const int pg = lane < boxes && j < u.hi ? pool_page(a.p, u.b, j) : -1;
+        // pool pages of this unit, 32 boxes' worth a batch, a lane each: the batch that values are taken from
+        // and the next, which keys may be ahead in
+        const int per = BN / R, batch = 32 / per;  // boxes of a tile, tiles of a batch (4 to 32)
+        auto look = [&](int x) {
+            const int j = u.lo + (32 * x + lane) * R, pg = j < u.hi ? pool_page(a.p, u.b, j) : -1;
             return pg < 0 ? a.p.pages : pg;  // past the last page: zeros
         };
-        int t;
-        bool is_v;
-        seq_tile(two_q, 0, tiles, t, is_v);
-        int pg = tiles > 0 ? look(t) : 0;
+        int pages_even = look(0), pages_odd = look(1);
         for (int seq = 0; seq < 2 * tiles; ++seq) {
+            int t;
+            bool is_v;
             seq_tile(two_q, seq, tiles, t, is_v);
+            const int x = t / batch;
+            if (is_v && x > 0 && t % batch == 0) {
+                if (x & 1) pages_even = look(x + 1);
+                else pages_odd = look(x + 1);
+            }
+            const int pg = __shfl_sync(0xffffffffu, x & 1 ? pages_odd : pages_even, (t * per + sub) & 31);
             const int slot = seq % NB, j0 = u.lo + t * BN;
             unsigned long long *full = KV8 ? &bar.raw_full[slot % 4] : is_v && t == tiles - 1 ? &bar.last_v : &bar.full[slot];
             unsigned long long *empty = KV8 ? &bar.raw_empty[slot % 4] : &bar.empty[slot];
@@ -266,17 +277,13 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                 tma_load_3d(dst, is_v ? &mv : &mk, half * 64, u.h * page + ((j0 + sub * R) & (page - 1)), pg, full);
             }
             issued = seq + 1;
-            if (seq + 1 < 2 * tiles) {
-                int t2;
-                bool v2;
-                seq_tile(two_q, seq + 1, tiles, t2, v2);
-                pg = look(t2);
-            }
         }
         if (*abort) {  // what was copied has to land before the CTA leaves
             if (tiles > 0) mbar_drain(&bar.q_full, 0);
             for (int seq = max(0, issued - NB); seq < issued; ++seq)
             {
+                int t;
+                bool is_v;
                 seq_tile(two_q, seq, tiles, t, is_v);
                 if (!KV8 && is_v && t == tiles - 1) mbar_drain(&bar.last_v, 0);
                 else mbar_drain(KV8 ? &bar.raw_full[seq % NB % 4] : &bar.full[seq % NB], (seq / NB) & 1);
@@ -311,14 +318,12 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                 if (!wait_one(&bar.p_full[j & 1], (j >> 1) & 1, abort)) return false;
                 tc_fence_after();
                 const uint64_t vd = v_desc + slot * (TILE / 16);
-                const uint32_t o = tm + 256 + (NS == 2 ? (j & 1) * 128 : 0);
+                const uint32_t o = tm + S::COL_O + (NS == 2 ? (j & 1) * S::O_STEP : 0), p = tm + S::COL_P + (j & 1) * S::P_STEP;
 #pragma unroll
-                for (int k = 0; k < BN / 16; ++k) umma_ts(o, tm + (j & 1) * BN + 8 * k, vd + k * (2048 / 16), id_o, k > 0 || j >= NS);
-                if (D != 128) umma_commit(&bar.pv);
+                for (int k = 0; k < BN / 16; ++k) umma_ts(o, p + 8 * k, vd + k * (2048 / 16), id_o, k > 0 || j >= NS);
+                if (NS == 1) umma_commit(&bar.pv);
                 if (!two_q || (j & 1)) umma_commit(&bar.empty[slot]);
-                // S(j + 2) overwrites P(j): products of one shape follow each other in order, of two shapes
-                // (D other than 128) the overwriting one is issued after the reading one is complete
-                return !(D != 128 && j + 2 < steps) || wait_one(&bar.pv, j & 1, abort);
+                return true;
             };
             ok = ok && scores(0);
             if (ok && steps > 1) ok = scores(1);
@@ -436,45 +441,51 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             ok = wait_for(&bar.q_full, 0, abort);
             if (two_q || s == 0) {
                 unsigned char *mine = smem + (two_q ? s * S::QTILE : 0) + row * 128;
+                constexpr int N = 8 * S::HALVES < 16 ? 8 * S::HALVES : 16;  // chunks held at a time
                 float big = 0.f;
-#pragma unroll 4
-                for (int x = 0; x < 8 * S::HALVES; ++x) {
-                    const uint4 w = *reinterpret_cast<const uint4 *>(mine + x / 8 * (128 * 128) + ((x + row) & 7) * 16);
-                    const unsigned v[4] = {w.x, w.y, w.z, w.w};
+                uint4 w[N];
+#pragma unroll 1
+                for (int x0 = 8 * S::HALVES - N; x0 >= 0; x0 -= N)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 f = unpack2<true>(v[e]);
-                        big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    for (int x = 0; x < N; ++x) {
+                        w[x] = *reinterpret_cast<const uint4 *>(mine + (x0 + x) / 8 * (128 * 128) + ((x + row) & 7) * 16);
+                        const unsigned v[4] = {w[x].x, w[x].y, w[x].z, w[x].w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 f = unpack2<true>(v[e]);
+                            big = fmaxf(big, fmaxf(fabsf(f.x), fabsf(f.y)));
+                        }
                     }
-                }
                 const int e2 = min(max((int)(__float_as_uint(big) >> 23) - 127, -126), 126);
                 const float f2 = __int_as_float((127 - e2) << 23);
-                bar.q_exp[r_unit] = (signed char)e2;
-#pragma unroll 4
-                for (int x = 0; x < 8 * S::HALVES; ++x) {
-                    uint4 *at = reinterpret_cast<uint4 *>(mine + x / 8 * (128 * 128) + ((x + row) & 7) * 16);
-                    const uint4 w = *at;
-                    unsigned v[4] = {w.x, w.y, w.z, w.w};
+                bar.q_exp[two_q ? tid : row] = (signed char)e2;
+#pragma unroll 1
+                for (int x0 = 0; x0 < 8 * S::HALVES; x0 += N)  // (the first ones are still held)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 f = unpack2<true>(v[e]);
-                        v[e] = pack2<false>(f.x * f2, f.y * f2);
+                    for (int x = 0; x < N; ++x) {
+                        uint4 *at = reinterpret_cast<uint4 *>(mine + (x0 + x) / 8 * (128 * 128) + ((x + row) & 7) * 16);
+                        const uint4 y = x0 ? *at : w[x];
+                        unsigned v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 f = unpack2<true>(v[e]);
+                            v[e] = pack2<false>(f.x * f2, f.y * f2);
+                        }
+                        *at = make_uint4(v[0], v[1], v[2], v[3]);
                     }
-                    *at = make_uint4(v[0], v[1], v[2], v[3]);
-                }
                 fence_proxy_async();
             }
             mbar_arrive(&bar.q_ready);
             bar_sync(1, S::SOFTMAX);
-            q_factor *= __int_as_float((127 + bar.q_exp[r_unit]) << 23);
+            q_factor *= __int_as_float((127 + bar.q_exp[two_q ? tid : row]) << 23);
         }
         const uint32_t lanes = (uint32_t)(32 * (warp % 4)) << 16;
-        const uint32_t o_addr = tm + lanes + 256 + (NS == 2 ? s * 128 : 0);
+        const uint32_t o_addr = tm + lanes + S::COL_O + (NS == 2 ? s * S::O_STEP : 0);
         float m = -INFINITY, l = 0.f;
         int ref = 0;
         for (int j = NS == 2 ? s : 0; ok && j < steps; j += NS) {
             const int t = two_q ? j >> 1 : j, j0 = u.lo + t * BN;
-            const uint32_t s_addr = tm + lanes + (j & 1) * BN;
+            const uint32_t s_addr = tm + lanes + (j & 1) * BN, p_addr = tm + lanes + S::COL_P + (j & 1) * S::P_STEP;
             if (!wait_for(&bar.s_full[j & 1], (j >> 1) & 1, abort)) { ok = false; break; }
             tc_fence_after();
             uint32_t x[BN / 32][32];
@@ -550,7 +561,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                     l2[(e >> 1) & 1] = __fadd2_rn(l2[(e >> 1) & 1], y);
                     p[e / 2] = pack2<MB>(y.x, y.y);
                 }
-                tmem_st16(s_addr + 16 * i, p);
+                tmem_st16(p_addr + 16 * i, p);
             }
             l += (l2[0].x + l2[1].x) + (l2[0].y + l2[1].y);
             tmem_wait_st();
@@ -562,8 +573,9 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
         tc_fence_after();
         const float unit = KV8 ? ex2((float)(ref - 127)) : 1.f;
         constexpr int PITCH = D + 4;
-        float *mo = reinterpret_cast<float *>(ring);
-        float2 *ml = reinterpret_cast<float2 *>(ring + 128 * PITCH * 4);
+        unsigned char *mine = ring + 8192;  // (the first bytes may hold rows on their way out)
+        float *mo = reinterpret_cast<float *>(mine);
+        float2 *ml = reinterpret_cast<float2 *>(mine + 128 * PITCH * 4);
         const bool merge = NS == 2 && !two_q;
         if (merge) {
             if (ok && s == 1) {
@@ -604,22 +616,23 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             const int at = (u.s + tok) * (a.p.heads * a.G) + u.h * a.G + (row0 + r_unit - tok * a.G);
             float *part = a.part + (size_t)(u.slot + u.c) * a.M * (D + 2);
             const bool bf = KV8 ? io_bf : BF;
-            // A warp's 32 rows x 32 columns pass through shared memory (the q tiles' place), so that eight lanes
+            // A warp's 32 rows x 64 columns pass through shared memory (the q tiles' place), so that 16 lanes
             // write a row's neighbouring columns; a lane writing its own row would touch 32 lines a store.
-            float *stage = reinterpret_cast<float *>(smem) + warp * (32 * 36);
+            float *stage = reinterpret_cast<float *>(smem) + warp * (32 * 68);
 #pragma unroll 1
-            for (int d = 0; d < D; d += 32) {
-                uint32_t y[1][32];
-                float z[32];
+            for (int d = 0; d < D; d += 64) {
+                uint32_t y[2][32];
+                float z[64];
                 if (any) {
                     tmem_ld32_start(o_addr + d, y[0]);
+                    tmem_ld32_start(o_addr + d + 32, y[1]);
                     tmem_wait_ld(y);
                 }
 #pragma unroll
-                for (int e = 0; e < 32; ++e) z[e] = any ? f0 * __uint_as_float(y[0][e]) : 0.f;
+                for (int e = 0; e < 64; ++e) z[e] = any ? f0 * __uint_as_float(y[e / 32][e % 32]) : 0.f;
                 if (other) {
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) {
+                    for (int e = 0; e < 64; e += 4) {
                         const float4 w = *reinterpret_cast<const float4 *>(mo + row * PITCH + d + e);
                         z[e] = fmaf(f1, w.x, z[e]);
                         z[e + 1] = fmaf(f1, w.y, z[e + 1]);
@@ -628,13 +641,13 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                     }
                 }
 #pragma unroll
-                for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4 *>(stage + lane * 36 + e) = make_float4(z[e], z[e + 1], z[e + 2], z[e + 3]);
+                for (int e = 0; e < 64; e += 4) *reinterpret_cast<float4 *>(stage + lane * 68 + e) = make_float4(z[e], z[e + 1], z[e + 2], z[e + 3]);
                 __syncwarp();
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int r = 4 * i + lane / 8, e = 4 * (lane % 8), ru = r_unit - lane + r;
+#pragma unroll 8
+                for (int i = 0; i < 16; ++i) {
+                    const int r = 2 * i + lane / 16, e = 4 * (lane % 16), ru = r_unit - lane + r;
                     const int row_at = __shfl_sync(0xffffffffu, at, r), r_tile = row - lane + r;
-                    const float4 w = *reinterpret_cast<const float4 *>(stage + r * 36 + e);
+                    const float4 w = *reinterpret_cast<const float4 *>(stage + r * 68 + e);
                     if (r_tile >= mq_rows || ru >= rows) continue;
                     if (final) {
                         uint2 h;
