@@ -107,6 +107,11 @@ __device__ __forceinline__ void tma_load_3d(void *smem, const void *tmap, int c0
                  " [%0], [%1, {%2, %3, %4}], [%5];"
                  :: "r"(smem_addr(smem)), "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(mb)) : "memory");
 }
+__device__ __forceinline__ void tma_load_2d(void *smem, const void *tmap, int c0, int c1, unsigned long long *mb) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3}], [%4];"
+                 :: "r"(smem_addr(smem)), "l"(tmap), "r"(c0), "r"(c1), "r"(smem_addr(mb)) : "memory");
+}
 __device__ __forceinline__ void mbar_arrive(unsigned long long *mb) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_addr(mb)) : "memory");
 }
@@ -146,13 +151,17 @@ struct TileShape {
     static constexpr int RAW = KV8 ? BN * D : 0;     // bytes of an 8-bit tile
     static constexpr int RAWS = KV8 ? (D == 64 ? 4 : 3) : 0;
     static constexpr int SOFTMAX = 128 * NS;         // threads of the softmax warpgroups
-    static constexpr int THREADS = SOFTMAX + 128 + (KV8 ? 128 : 0);
+    // warps that turn 8-bit tiles into fp16: two beside the producer's and the products' warp, and the rest
+    static constexpr int CVT = KV8 ? (D == 256 ? 320 : 192) : 0;
+    static constexpr int THREADS = SOFTMAX + 128 + (KV8 ? CVT - 64 : 0);
     // columns of tensor memory: S at 0 and BN, P in the place of S for D = 128 (where that fills the
     // 512 columns), else beside it
     static constexpr int COL_P = D == 128 ? 0 : D == 64 ? 384 : 128, P_STEP = D == 128 ? BN : BN / 2, COL_O = 256, O_STEP = D;
     static constexpr int OFF_RING = NS * QTILE;
     static constexpr int OFF_RAW = OFF_RING + SLOTS * TILE;
-    static constexpr int OFF_BAR = OFF_RAW + RAWS * RAW;
+    // [RAWS][2][8][128]: exponent bytes of a key tile's keys and values, 128 bytes (a copy's alignment) a page
+    static constexpr int OFF_EXP = OFF_RAW + RAWS * RAW;
+    static constexpr int OFF_BAR = OFF_EXP + RAWS * 2048;
     static constexpr int BYTES = OFF_BAR + 1024 + 1024;                        // and the alignment of the base
     static_assert(BYTES <= 232448, "shared memory of one CTA");
     static_assert(NS == 1 || 8192 + 128 * (D + 4) * 4 + 1024 <= SLOTS * TILE, "the streams merge in the ring");
@@ -182,24 +191,25 @@ __device__ __forceinline__ void seq_tile(bool two_q, int seq, int n, int &t, boo
 template <int D, bool BF, bool KV8>
 __global__ void __launch_bounds__(TileShape<D, KV8>::THREADS, 1)
 attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap mq,
-                 const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, bool io_bf) {
+                 const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
+                 const __grid_constant__ CUtensorMap mke, const __grid_constant__ CUtensorMap mve, bool io_bf) {
     using S = TileShape<D, KV8>;
     constexpr int BN = S::BN, NS = S::NS, SLOTS = S::SLOTS, TILE = S::TILE;
     constexpr bool MB = BF && !KV8;
     constexpr int W_TMA = S::SOFTMAX / 32, W_MMA = W_TMA + 1;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    unsigned char *ring = smem + S::OFF_RING, *raw = smem + S::OFF_RAW;
+    unsigned char *ring = smem + S::OFF_RING, *raw = smem + S::OFF_RAW, *exps = smem + S::OFF_EXP;
     Bars &bar = *reinterpret_cast<Bars *>(smem + S::OFF_BAR);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     if (tid == 0) {
         for (int i = 0; i < SLOTS; ++i) {
-            mbar_init(&bar.full[i], KV8 ? 128 : 1);
+            mbar_init(&bar.full[i], KV8 ? S::CVT : 1);
             mbar_init(&bar.empty[i], 1);
         }
         for (int i = 0; i < S::RAWS; ++i) {
             mbar_init(&bar.raw_full[i], 1);
-            mbar_init(&bar.raw_empty[i], 128);
+            mbar_init(&bar.raw_empty[i], S::CVT);
         }
         for (int i = 0; i < 4; ++i) mbar_init(&bar.ref_full[i], 1);
         for (int i = 0; i < 2; ++i) {
@@ -270,11 +280,16 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             unsigned long long *full = KV8 ? &bar.raw_full[slot % 4] : is_v && t == tiles - 1 ? &bar.last_v : &bar.full[slot];
             unsigned long long *empty = KV8 ? &bar.raw_empty[slot % 4] : &bar.empty[slot];
             if (seq >= NB && !wait_for(empty, ((seq / NB) - 1) & 1, abort)) break;
-            if (lane == 0) mbar_arrive_expect_tx(full, KV8 ? S::RAW : TILE);
+            if (lane == 0) mbar_arrive_expect_tx(full, KV8 ? S::RAW + (is_v ? 0 : 2 * BN) : TILE);
             __syncwarp();
             if (lane < boxes) {
                 unsigned char *dst = KV8 ? raw + slot * S::RAW + sub * R * D : ring + slot * TILE + half * BN * 128 + sub * R * 128;
-                tma_load_3d(dst, is_v ? &mv : &mk, half * 64, u.h * page + ((j0 + sub * R) & (page - 1)), pg, full);
+                const int y = u.h * page + ((j0 + sub * R) & (page - 1));
+                tma_load_3d(dst, is_v ? &mv : &mk, half * 64, y, pg, full);
+                if (KV8 && !is_v) {
+                    tma_load_2d(exps + slot * 2048 + sub * 128, &mke, y, pg, full);
+                    tma_load_2d(exps + slot * 2048 + 1024 + sub * 128, &mve, y, pg, full);
+                }
             }
             issued = seq + 1;
         }
@@ -335,9 +350,9 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             if (!ok) mbar_drain(&bar.fin, 0);
         }
         __syncwarp();
-    } else if (warp >= W_TMA && warp < W_TMA + 4) {
+    } else if (!KV8 && warp >= W_TMA) {
         if (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        if (!KV8 && warp == W_TMA + 2 && tiles > 0) {
+        if (warp == W_TMA + 2 && tiles > 0) {
             // ---- the last tile's values past the range; its copy lands on a barrier of its own
             const int slot = seq_v(two_q, tiles - 1, tiles) % SLOTS, live = u.hi - (u.lo + (tiles - 1) * BN);
             if (wait_for(&bar.last_v, 0, abort)) {
@@ -350,31 +365,18 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                 if (lane == 0) mbar_arrive(&bar.full[slot]);
             }
         }
-    } else if (KV8 && warp >= W_TMA + 4) {
+    } else if (KV8 && warp >= W_TMA) {
         if (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         // ---- 8-bit tiles to fp16
-        const int c = tid - (W_TMA + 4) * 32;
+        const int c = tid - (W_TMA + 2) * 32;
+        const int sub_log2 = min(a.p.page_shift, BN == 128 ? 7 : 6), sub_rows = 1 << sub_log2;  // tokens of a box
         int ref[2] = {0, 0}, ref_most = 0;  // the values' R of the last two tiles
+        unsigned evs[2] = {0, 0};           // and their exponents, of tokens 4 lane .. + 3 (in every warp)
         for (int seq = 0; seq < 2 * tiles; ++seq) {
             int t;
             bool is_v;
             seq_tile(two_q, seq, tiles, t, is_v);
-            const int j0 = u.lo + t * BN, live = min(BN, u.hi - j0);
-            // exponents of tokens 4 lane .. + 3, by every warp for itself (in the shadow of the waits)
-            unsigned ek = 0, ev = 0;
-            if (4 * lane < live) {
-                const int pg = pool_page(a.p, u.b, j0 + 4 * lane);
-                if (pg >= 0) {
-                    const long long at = ((((long long)pg * a.p.heads + u.h)) << a.p.page_shift) + ((j0 + 4 * lane) & ((1 << a.p.page_shift) - 1));
-                    ev = __ldg(reinterpret_cast<const unsigned *>(a.ve + at));
-                    if (!is_v) ek = __ldg(reinterpret_cast<const unsigned *>(a.ke + at));
-                    if (live - 4 * lane < 4) {  // bytes past the range are not the request's
-                        const unsigned mask = (1u << (8 * (live - 4 * lane))) - 1u;
-                        ek &= mask;
-                        ev &= mask;
-                    }
-                }
-            }
+            const int live = min(BN, u.hi - (u.lo + t * BN));
             const int slot = seq % SLOTS, rs = seq % (KV8 ? S::RAWS : 1);
             if (seq >= SLOTS && !wait_for(&bar.empty[slot], ((seq / SLOTS) - 1) & 1, abort)) break;
             if (!wait_for(&bar.raw_full[rs], (seq / (KV8 ? S::RAWS : 1)) & 1, abort)) break;
@@ -383,10 +385,21 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                 return (int)__reduce_max_sync(0xffffffffu, max(m & 0xffu, (m >> 8) & 0xffu));
             };
             int R;
+            unsigned e4;
             if (!is_v) {  // with the keys, the softmax learns both
-                R = largest(ek);
+                const bool here = 4 * lane < live;
+                const unsigned char *at = exps + rs * 2048 + (4 * lane >> sub_log2) * 128 + (4 * lane & (sub_rows - 1));
+                unsigned ev = here ? *reinterpret_cast<const unsigned *>(at + 1024) : 0;
+                e4 = here ? *reinterpret_cast<const unsigned *>(at) : 0;
+                if (here && live - 4 * lane < 4) {  // bytes past the range are not the request's
+                    const unsigned mask = (1u << (8 * (live - 4 * lane))) - 1u;
+                    e4 &= mask;
+                    ev &= mask;
+                }
+                R = largest(e4);
                 ref_most = max(ref_most, largest(ev));
                 (t & 1 ? ref[1] : ref[0]) = ref_most;
+                (t & 1 ? evs[1] : evs[0]) = ev;
                 if (c == 0) {
                     bar.k_ref[t & 3] = R;
                     bar.v_ref[t & 3] = ref_most;
@@ -394,16 +407,18 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                 }
             } else {
                 R = t & 1 ? ref[1] : ref[0];
+                e4 = t & 1 ? evs[1] : evs[0];
             }
-            const unsigned e4 = is_v ? ev : ek;
             const unsigned char *src = raw + rs * S::RAW;
             unsigned char *dst = ring + slot * TILE;
-#pragma unroll 4
-            for (int i = 0; i < BN * D / 16 / 128; ++i) {
-                const int x = i * 128 + c, r = x / (D / 16), e = x % (D / 16) * 16, half = e / 64, ch = e % 64 / 8;
+            constexpr int CHUNKS = BN * D / 16, PER = KV8 ? (CHUNKS + S::CVT - 1) / (KV8 ? S::CVT : 1) : 1;
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int x = i * S::CVT + c, r = x / (D / 16), e = x % (D / 16) * 16, half = e / 64, ch = e % 64 / 8;
                 // 2^(E - R) in fp16: subnormal below 2^-14, zero below 2^-24; rows past the range are zeros
-                const int E = (int)((__shfl_sync(0xffffffffu, e4, r / 4) >> (8 * (r & 3))) & 0xffu) - R;
+                const int E = (int)((__shfl_sync(0xffffffffu, e4, (r / 4) & 31) >> (8 * (r & 3))) & 0xffu) - R;
                 const __half2 f = __float2half2_rn(__int_as_float(max(E + 127, 0) << 23));
+                if (x >= CHUNKS) break;  // (a warp's 32 chunks at once)
                 uint4 w = *reinterpret_cast<const uint4 *>(src + x * 16);
                 if (r >= live) w = make_uint4(0, 0, 0, 0);
                 auto two = [&](unsigned v) {
@@ -699,14 +714,26 @@ bool q_map(CUtensorMap *m, const AttnArgs &a, int D) {
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// [pages][heads * page] exponent bytes: boxes of `rows` bytes, zeros past the last page.
+bool exp_map(CUtensorMap *m, const void *base, const AttnArgs &a, int rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t row = (cuuint64_t)a.p.heads << a.p.page_shift;
+    const cuuint64_t dims[2] = {row, (cuuint64_t)a.p.pages}, strides[1] = {row};
+    const cuuint32_t box[2] = {(cuuint32_t)rows, 1}, es[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int D, bool BF, bool KV8>
 dn_status launch_tile(const AttnArgs &a, bool io_bf, unsigned grid, cudaStream_t st) {
     using S = TileShape<D, KV8>;
     const int rows = 1 << a.p.page_shift < S::BN ? 1 << a.p.page_shift : S::BN;
-    CUtensorMap mq, mk, mv;
+    CUtensorMap mq, mk, mv, mke = {}, mve = {};
     if (!q_map(&mq, a, D) || !pool_map(&mk, a.kc, a, D, KV8 ? 1 : 2, rows) || !pool_map(&mv, a.vc, a, D, KV8 ? 1 : 2, rows)) return DN_ERR_CUDA;
+    if (KV8 && (!exp_map(&mke, a.ke, a, rows) || !exp_map(&mve, a.ve, a, rows))) return DN_ERR_CUDA;
     cudaFuncSetAttribute(attn_tile_kernel<D, BF, KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
-    launch_pdl(attn_tile_kernel<D, BF, KV8>, dim3(grid), dim3(S::THREADS), S::BYTES, st, a, mq, mk, mv, io_bf);
+    launch_pdl(attn_tile_kernel<D, BF, KV8>, dim3(grid), dim3(S::THREADS), S::BYTES, st, a, mq, mk, mv, mke, mve, io_bf);
     return DN_OK;
 }
 
