@@ -151,15 +151,16 @@ struct TileShape {
     static constexpr int RAW = KV8 ? BN * D : 0;     // bytes of an 8-bit tile
     static constexpr int RAWS = KV8 ? (D == 64 ? 4 : 3) : 0;
     static constexpr int SOFTMAX = 128 * NS;         // threads of the softmax warpgroups
-    // warps that turn 8-bit tiles into fp16: two beside the producer's and the products' warp, and the rest
-    static constexpr int CVT = KV8 ? (D == 256 ? 320 : 192) : 0;
-    static constexpr int THREADS = SOFTMAX + 128 + (KV8 ? CVT - 64 : 0);
+    // threads that turn 8-bit tiles into fp16, half of them the keys and half the values (so that one's waits
+    // pass beside the other's work): two warps beside the producer's and the products' warp, and the rest
+    static constexpr int CVT = KV8 ? (D == 256 ? 160 : 96) : 0;
+    static constexpr int THREADS = SOFTMAX + 128 + (KV8 ? 2 * CVT - 64 : 0);
     // columns of tensor memory: S at 0 and BN, P in the place of S for D = 128 (where that fills the
     // 512 columns), else beside it
     static constexpr int COL_P = D == 128 ? 0 : D == 64 ? 384 : 128, P_STEP = D == 128 ? BN : BN / 2, COL_O = 256, O_STEP = D;
     static constexpr int OFF_RING = NS * QTILE;
     static constexpr int OFF_RAW = OFF_RING + SLOTS * TILE;
-    // [RAWS][2][8][128]: exponent bytes of a key tile's keys and values, 128 bytes (a copy's alignment) a page
+    // [RAWS][2][8][128]: exponent bytes of a tile's keys and values (values alone with the values), 128 bytes (a copy's alignment) a page
     static constexpr int OFF_EXP = OFF_RAW + RAWS * RAW;
     static constexpr int OFF_BAR = OFF_EXP + RAWS * 2048;
     static constexpr int BYTES = OFF_BAR + 1024 + 1024;                        // and the alignment of the base
@@ -168,7 +169,8 @@ struct TileShape {
 };
 
 struct Bars {
-    unsigned long long full[8], empty[8], raw_full[4], raw_empty[4], ref_full[4], s_full[2], p_full[2], pv, q_full, q_ready, last_v, fin;
+    // by kind (keys, values) and tile modulo 4: a ring is at most eight slots, so four tiles, ahead
+    unsigned long long full[2][4], empty[2][4], raw_full[2][4], raw_empty[2][4], ref_full[4], s_full[2], p_full[2], pv, q_full, q_ready, last_v, fin;
     uint32_t tmem;
     int abort, k_ref[4], v_ref[4];
     signed char q_exp[256];  // powers of two of bf16 q rows brought to fp16
@@ -203,13 +205,11 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
     Bars &bar = *reinterpret_cast<Bars *>(smem + S::OFF_BAR);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     if (tid == 0) {
-        for (int i = 0; i < SLOTS; ++i) {
-            mbar_init(&bar.full[i], KV8 ? S::CVT : 1);
-            mbar_init(&bar.empty[i], 1);
-        }
-        for (int i = 0; i < S::RAWS; ++i) {
-            mbar_init(&bar.raw_full[i], 1);
-            mbar_init(&bar.raw_empty[i], S::CVT);
+        for (int i = 0; i < 8; ++i) {
+            mbar_init(&bar.full[i >> 2][i & 3], KV8 ? S::CVT : 1);
+            mbar_init(&bar.empty[i >> 2][i & 3], 1);
+            mbar_init(&bar.raw_full[i >> 2][i & 3], 1);
+            mbar_init(&bar.raw_empty[i >> 2][i & 3], KV8 ? S::CVT : 1);
         }
         for (int i = 0; i < 4; ++i) mbar_init(&bar.ref_full[i], 1);
         for (int i = 0; i < 2; ++i) {
@@ -277,17 +277,21 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             }
             const int pg = __shfl_sync(0xffffffffu, x & 1 ? pages_odd : pages_even, (t * per + sub) & 31);
             const int slot = seq % NB, j0 = u.lo + t * BN;
-            unsigned long long *full = KV8 ? &bar.raw_full[slot % 4] : is_v && t == tiles - 1 ? &bar.last_v : &bar.full[slot];
-            unsigned long long *empty = KV8 ? &bar.raw_empty[slot % 4] : &bar.empty[slot];
-            if (seq >= NB && !wait_for(empty, ((seq / NB) - 1) & 1, abort)) break;
-            if (lane == 0) mbar_arrive_expect_tx(full, KV8 ? S::RAW + (is_v ? 0 : 2 * BN) : TILE);
+            unsigned long long *full = KV8 ? &bar.raw_full[is_v][t & 3] : is_v && t == tiles - 1 ? &bar.last_v : &bar.full[is_v][t & 3];
+            if (seq >= NB) {  // what was in the slot before
+                int t0;
+                bool v0;
+                seq_tile(two_q, seq - NB, tiles, t0, v0);
+                if (!wait_for(KV8 ? &bar.raw_empty[v0][t0 & 3] : &bar.empty[v0][t0 & 3], (t0 >> 2) & 1, abort)) break;
+            }
+            if (lane == 0) mbar_arrive_expect_tx(full, KV8 ? S::RAW + (is_v ? BN : 2 * BN) : TILE);
             __syncwarp();
             if (lane < boxes) {
                 unsigned char *dst = KV8 ? raw + slot * S::RAW + sub * R * D : ring + slot * TILE + half * BN * 128 + sub * R * 128;
                 const int y = u.h * page + ((j0 + sub * R) & (page - 1));
                 tma_load_3d(dst, is_v ? &mv : &mk, half * 64, y, pg, full);
-                if (KV8 && !is_v) {
-                    tma_load_2d(exps + slot * 2048 + sub * 128, &mke, y, pg, full);
+                if (KV8) {
+                    if (!is_v) tma_load_2d(exps + slot * 2048 + sub * 128, &mke, y, pg, full);
                     tma_load_2d(exps + slot * 2048 + 1024 + sub * 128, &mve, y, pg, full);
                 }
             }
@@ -301,7 +305,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                 bool is_v;
                 seq_tile(two_q, seq, tiles, t, is_v);
                 if (!KV8 && is_v && t == tiles - 1) mbar_drain(&bar.last_v, 0);
-                else mbar_drain(KV8 ? &bar.raw_full[seq % NB % 4] : &bar.full[seq % NB], (seq / NB) & 1);
+                else mbar_drain(KV8 ? &bar.raw_full[is_v][t & 3] : &bar.full[is_v][t & 3], (t >> 2) & 1);
             }
         }
     } else if (warp == W_MMA) {
@@ -317,19 +321,19 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                            v_desc = desc_mnmajor(smem_addr(ring), BN * 128);
             auto scores = [&](int j) {
                 const int t = two_q ? j >> 1 : j, seq = seq_k(two_q, t), slot = seq % SLOTS;
-                if (!wait_one(&bar.full[slot], (seq / SLOTS) & 1, abort)) return false;
+                if (!wait_one(&bar.full[0][t & 3], (t >> 2) & 1, abort)) return false;
                 tc_fence_after();
                 const uint64_t qd = q_desc + (two_q ? (j & 1) * (S::QTILE / 16) : 0), kd = k_desc + slot * (TILE / 16);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
                     umma_f16(tm + (j & 1) * BN, qd + (k / 4) * (128 * 128 / 16) + (k % 4) * 2, kd + (k / 4) * (BN * 128 / 16) + (k % 4) * 2, id_s, k > 0);
                 umma_commit(&bar.s_full[j & 1]);
-                if (!two_q || (j & 1)) umma_commit(&bar.empty[slot]);
+                if (!two_q || (j & 1)) umma_commit(&bar.empty[0][t & 3]);
                 return true;
             };
             auto outputs = [&](int j) {
                 const int t = two_q ? j >> 1 : j, seq = seq_v(two_q, t, tiles), slot = seq % SLOTS;
-                if (!wait_one(&bar.full[slot], (seq / SLOTS) & 1, abort)) return false;
+                if (!wait_one(&bar.full[1][t & 3], (t >> 2) & 1, abort)) return false;
                 if (!wait_one(&bar.p_full[j & 1], (j >> 1) & 1, abort)) return false;
                 tc_fence_after();
                 const uint64_t vd = v_desc + slot * (TILE / 16);
@@ -337,7 +341,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
 #pragma unroll
                 for (int k = 0; k < BN / 16; ++k) umma_ts(o, p + 8 * k, vd + k * (2048 / 16), id_o, k > 0 || j >= NS);
                 if (NS == 1) umma_commit(&bar.pv);
-                if (!two_q || (j & 1)) umma_commit(&bar.empty[slot]);
+                if (!two_q || (j & 1)) umma_commit(&bar.empty[1][t & 3]);
                 return true;
             };
             ok = ok && scores(0);
@@ -362,52 +366,43 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                 }
                 fence_proxy_async();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.full[slot]);
+                if (lane == 0) mbar_arrive(&bar.full[1][(tiles - 1) & 3]);
             }
         }
     } else if (KV8 && warp >= W_TMA) {
         if (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         // ---- 8-bit tiles to fp16
-        const int c = tid - (W_TMA + 2) * 32;
+        const int group = tid - (W_TMA + 2) * 32 >= S::CVT, c = tid - (W_TMA + 2) * 32 - (group ? S::CVT : 0);  // 0: keys, 1: values
         const int sub_log2 = min(a.p.page_shift, BN == 128 ? 7 : 6), sub_rows = 1 << sub_log2;  // tokens of a box
-        int ref[2] = {0, 0}, ref_most = 0;  // the values' R of the last two tiles
-        unsigned evs[2] = {0, 0};           // and their exponents, of tokens 4 lane .. + 3 (in every warp)
-        for (int seq = 0; seq < 2 * tiles; ++seq) {
-            int t;
-            bool is_v;
-            seq_tile(two_q, seq, tiles, t, is_v);
-            const int live = min(BN, u.hi - (u.lo + t * BN));
+        int ref_most = 0;
+        for (int t = 0; t < tiles; ++t) {
+            const bool is_v = group;
+            const int seq = is_v ? seq_v(two_q, t, tiles) : seq_k(two_q, t), live = min(BN, u.hi - (u.lo + t * BN));
             const int slot = seq % SLOTS, rs = seq % (KV8 ? S::RAWS : 1);
-            if (seq >= SLOTS && !wait_for(&bar.empty[slot], ((seq / SLOTS) - 1) & 1, abort)) break;
-            if (!wait_for(&bar.raw_full[rs], (seq / (KV8 ? S::RAWS : 1)) & 1, abort)) break;
+            if (!wait_for(&bar.raw_full[is_v][t & 3], (t >> 2) & 1, abort)) break;
+            // exponents of tokens 4 lane .. + 3, in every warp; bytes past the range are not the request's
+            const bool here = 4 * lane < live;
+            const unsigned mask = live - 4 * lane >= 4 ? 0xffffffffu : here ? (1u << (8 * (live - 4 * lane))) - 1u : 0u;
+            const unsigned char *at = exps + rs * 2048 + (4 * lane >> sub_log2) * 128 + (4 * lane & (sub_rows - 1));
+            const unsigned ev = here ? *reinterpret_cast<const unsigned *>(at + 1024) & mask : 0;
+            const unsigned ek = here && !is_v ? *reinterpret_cast<const unsigned *>(at) & mask : 0;
             auto largest = [](unsigned e) {
                 const unsigned m = __vmaxu4(e, e >> 16);
                 return (int)__reduce_max_sync(0xffffffffu, max(m & 0xffu, (m >> 8) & 0xffu));
             };
-            int R;
-            unsigned e4;
-            if (!is_v) {  // with the keys, the softmax learns both
-                const bool here = 4 * lane < live;
-                const unsigned char *at = exps + rs * 2048 + (4 * lane >> sub_log2) * 128 + (4 * lane & (sub_rows - 1));
-                unsigned ev = here ? *reinterpret_cast<const unsigned *>(at + 1024) : 0;
-                e4 = here ? *reinterpret_cast<const unsigned *>(at) : 0;
-                if (here && live - 4 * lane < 4) {  // bytes past the range are not the request's
-                    const unsigned mask = (1u << (8 * (live - 4 * lane))) - 1u;
-                    e4 &= mask;
-                    ev &= mask;
-                }
-                R = largest(e4);
-                ref_most = max(ref_most, largest(ev));
-                (t & 1 ? ref[1] : ref[0]) = ref_most;
-                (t & 1 ? evs[1] : evs[0]) = ev;
-                if (c == 0) {
-                    bar.k_ref[t & 3] = R;
-                    bar.v_ref[t & 3] = ref_most;
-                    mbar_arrive(&bar.ref_full[t & 3]);
-                }
-            } else {
-                R = t & 1 ? ref[1] : ref[0];
-                e4 = t & 1 ? evs[1] : evs[0];
+            ref_most = max(ref_most, largest(ev));
+            const int R = is_v ? ref_most : largest(ek);
+            const unsigned e4 = is_v ? ev : ek;
+            if (seq >= SLOTS) {
+                int t0;
+                bool v0;
+                seq_tile(two_q, seq - SLOTS, tiles, t0, v0);
+                if (!wait_for(&bar.empty[v0][t0 & 3], (t0 >> 2) & 1, abort)) break;
+            }
+            if (!is_v && c == 0) {  // the softmax learns both with the keys (t - 4 is past when a slot is free for t)
+                bar.k_ref[t & 3] = R;
+                bar.v_ref[t & 3] = ref_most;
+                mbar_arrive(&bar.ref_full[t & 3]);
             }
             const unsigned char *src = raw + rs * S::RAW;
             unsigned char *dst = ring + slot * TILE;
@@ -435,8 +430,8 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                 *reinterpret_cast<uint4 *>(row + (((ch + 1 - first) ^ (r & 7)) << 4)) = first ? o[0] : o[1];
             }
             fence_proxy_async();
-            mbar_arrive(&bar.full[slot]);
-            mbar_arrive(&bar.raw_empty[rs]);
+            mbar_arrive(&bar.full[is_v][t & 3]);
+            mbar_arrive(&bar.raw_empty[is_v][t & 3]);
         }
     } else {
         // ---- softmax: a thread per row
