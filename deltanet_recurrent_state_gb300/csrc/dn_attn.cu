@@ -8,9 +8,9 @@
 //
 // attn_rows_kernel, here, is for few rows: tiles of 16 or 32 rows with warp MMAs. With so few rows the
 // cache is read once and used little, so the kernel is bound by those reads: each warp streams its own
-// 16-token pieces of the range through a private ring in shared memory (cp.async, XOR-swizzled
+// 16- or 32-token pieces of the range through a private ring in shared memory (cp.async, XOR-swizzled
 // chunks) and never waits for another warp until the end, where the warps' m, sums and outputs are
-// merged. Pages are multiples of 16 tokens, so a piece is one contiguous segment of the pool.
+// merged. Pages are multiples of 16 tokens, so 16 tokens are one contiguous segment of the pool.
 //
 // 8-bit caches. The e4m3 values go to fp16 in registers, exactly; the rows' powers of two never
 // touch them. A key's exponent multiplies its score in 32 bits. A value's exponent multiplies its
@@ -20,6 +20,7 @@
 // largest), so bf16 inputs take the same path. An 8x8 ldmatrix tile of bytes gives a thread four
 // neighbouring bytes of one row: for the keys the four are two k-pairs of the MMA (the same order is
 // used for q, and a dot product has no order), for the values they are two tokens' pairs of columns.
+#include <algorithm>
 #include <type_traits>
 
 #include <cuda_runtime.h>
@@ -58,15 +59,19 @@ __device__ __forceinline__ int chunk_at(int r, int c) {
     return CPR >= 8 ? r * CPR + (c ^ (r & 7)) : r * CPR + (c ^ ((r >> 1) & (CPR - 1)));
 }
 
-constexpr int kPiece = 16;  // tokens of a warp's step
-
 template <int D, int MT, bool KV8>
 struct RowsShape {
     static constexpr int W = 4;                               // warps
     static constexpr int EB = KV8 ? 1 : 2;                    // bytes of a cached element
-    static constexpr int TILE = kPiece * D * EB;              // bytes of one piece's keys
-    static constexpr int STAGE = 2 * TILE + (KV8 ? 32 : 0);   // keys, values, exponent bytes
-    static constexpr int ST = D * EB >= 512 ? 3 : 4;          // ring stages
+    // Tokens of a warp's step, in halves of 16 (a page is a multiple of that): 32 where 16 tokens are few
+    // bytes and the instructions of a step weigh (8 bits, D = 64), 16 where the ring would leave too few warps.
+    static constexpr int H = D * EB <= 128 ? 2 : 1, P = 16 * H;
+    static constexpr int HALF = 16 * D * EB;                  // bytes of 16 tokens' keys
+    static constexpr int TILE = H * HALF;
+    static constexpr int STAGE = 2 * TILE + (KV8 ? 32 * H : 0);   // keys, values, exponent bytes
+    // Ring stages. Two leave three CTAs an SM (96 KB in flight, and 12 warps to compute): with four, one CTA of
+    // 4 warps, the batch of 64 single tokens (D = 128, 16-bit) took 266 us instead of 193.
+    static constexpr int ST = D * EB >= 256 && !(D == 128) ? 3 : 2;
     static constexpr int M = 16 * MT;
     static constexpr bool QREG = D * MT <= 128;               // q fragments in registers, else shared
     static constexpr size_t RING = (size_t)W * ST * STAGE;
@@ -79,7 +84,7 @@ template <int D, int MT, bool BF, bool KV8>
 __global__ void __launch_bounds__(128)
 attn_rows_kernel(const __grid_constant__ AttnArgs a, bool io_bf) {
     using S = RowsShape<D, MT, KV8>;
-    constexpr int W = S::W, ST = S::ST, KS = D / 16, CPR = D * S::EB / 16, M = S::M;
+    constexpr int W = S::W, ST = S::ST, KS = D / 16, CPR = D * S::EB / 16, M = S::M, H = S::H, P = S::P;
     constexpr bool MB = BF && !KV8;  // type of the MMAs
     extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane >> 2, t4 = lane & 3;
@@ -90,29 +95,37 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a, bool io_bf) {
     if (u.c >= u.ranges) return;
     const int row0 = u.t * M, rows = min(M, u.n * a.G - row0);  // (the host bounds total * heads)
 
-    // ---- the ring: piece i of this warp is tokens lo + 16 (warp + W i) .. + 15 of the range
+    // ---- the ring: piece i of this warp is tokens lo + P (warp + W i) .. + P - 1 of the range
     unsigned char *ring = smem + (size_t)warp * ST * S::STAGE;
-    const int pieces = max(0, ((u.hi - u.lo + kPiece - 1) / kPiece - warp + W - 1) / W);
-    int page_ahead = -1;  // lane l: the pool page of this warp's piece 32 * batch + l
+    const int pieces = max(0, ((u.hi - u.lo + P - 1) / P - warp + W - 1) / W);
+    int page_ahead = -1;  // lane l: the pool page of this warp's 16 tokens number 32 * batch + l
     auto load = [&](int i) {
         if (i < pieces) {
-            if ((i & 31) == 0) page_ahead = pool_page(a.p, u.b, u.lo + kPiece * (warp + W * (i + lane)));
-            const int pg = __shfl_sync(0xffffffffu, page_ahead, i & 31);
-            const int j0 = u.lo + kPiece * (warp + W * i);
-            const long long row0 = ((((long long)max(pg, 0) * a.p.heads + u.h)) << a.p.page_shift) + (j0 & ((1 << a.p.page_shift) - 1));
-            const int live = pg < 0 ? 0 : min(kPiece, u.hi - j0);  // rows past the range are zeros
+            if (((i * H) & 31) == 0) page_ahead = pool_page(a.p, u.b, u.lo + P * (warp + W * (i + lane / H)) + 16 * (lane % H));
             unsigned char *st = ring + (i % ST) * S::STAGE;
-            const unsigned char *ks = static_cast<const unsigned char *>(a.kc) + row0 * (D * S::EB);
-            const unsigned char *vs = static_cast<const unsigned char *>(a.vc) + row0 * (D * S::EB);
 #pragma unroll
-            for (int x = 0; x < kPiece * CPR / 32; ++x) {
-                const int e = x * 32 + lane, r = e / CPR, at = 16 * chunk_at<CPR>(r, e % CPR);
-                const int bytes = r < live ? 16 : 0;
-                cp_async16(st + at, bytes ? ks + e * 16 : static_cast<const unsigned char *>(a.q), bytes);  // (nothing is read where bytes is 0)
-                cp_async16(st + S::TILE + at, bytes ? vs + e * 16 : static_cast<const unsigned char *>(a.q), bytes);
+            for (int h = 0; h < H; ++h) {
+                const int pg = __shfl_sync(0xffffffffu, page_ahead, (i * H + h) & 31);
+                const int j0 = u.lo + P * (warp + W * i) + 16 * h;
+                const long long row0 = ((((long long)max(pg, 0) * a.p.heads + u.h)) << a.p.page_shift) + (j0 & ((1 << a.p.page_shift) - 1));
+                const int live = pg < 0 ? 0 : min(16, u.hi - j0);  // rows past the range are zeros
+                const unsigned char *ks = static_cast<const unsigned char *>(a.kc) + row0 * (D * S::EB) + lane * 16;
+                const unsigned char *vs = static_cast<const unsigned char *>(a.vc) + row0 * (D * S::EB) + lane * 16;
+#pragma unroll
+                for (int x = 0; x < 16 * CPR / 32; ++x) {
+                    const int e = x * 32 + lane, at = h * S::HALF + 16 * chunk_at<CPR>(e / CPR, e % CPR);
+                    if (live >= 16) {
+                        cp_async16(st + at, ks + x * 512, 16);
+                        cp_async16(st + S::TILE + at, vs + x * 512, 16);
+                    } else {  // (nothing is read where the count is 0)
+                        const int bytes = e / CPR < live ? 16 : 0;
+                        cp_async16(st + at, bytes ? ks + x * 512 : static_cast<const unsigned char *>(a.q), bytes);
+                        cp_async16(st + S::TILE + at, bytes ? vs + x * 512 : static_cast<const unsigned char *>(a.q), bytes);
+                    }
+                }
+                if (KV8 && lane < 2)
+                    cp_async16(st + 2 * S::TILE + 32 * h + 16 * lane, live > 0 ? (lane ? a.ve : a.ke) + row0 : static_cast<const uint8_t *>(a.q), live > 0 ? 16 : 0);
             }
-            if (KV8 && lane < 2)
-                cp_async16(st + 2 * S::TILE + 16 * lane, live > 0 ? (lane ? a.ve : a.ke) + row0 : static_cast<const uint8_t *>(a.q), live > 0 ? 16 : 0);
         }
         cp_async_commit();
     };
@@ -213,65 +226,72 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a, bool io_bf) {
         __syncwarp();
         load(i + ST - 1);
         const unsigned char *st = ring + (i % ST) * S::STAGE;
-        const int j0 = u.lo + kPiece * (warp + W * i);
-        // ---- scores of 16 tokens
-        float s[MT][2][4];
+        const int j0 = u.lo + P * (warp + W * i);
+        // ---- scores
+        float s[MT][2 * H][4];
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int x = 0; x < 8; ++x) s[mt][x >> 2][x & 3] = 0.f;
+            for (int x = 0; x < 8 * H; ++x) s[mt][x >> 2][x & 3] = 0.f;
+        unsigned kb[H][4];  // 8 bits: key bytes of two k-steps
 #pragma unroll
         for (int ks = 0; ks < KS; ks += KV8 ? 2 : 1) {
-            unsigned r[4];
-            if (!KV8) {
-                // matrices: tokens 0-7 at k 0-7, k 8-15, tokens 8-15 at k 0-7, k 8-15
-                ldsm_x4(r, st + 16 * chunk_at<CPR>((lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1)));
-            } else {
-                // matrices: tokens 0-7, 8-15 at bytes 16 ks .., then at bytes 16 (ks + 1) ..
-                ldsm_x4(r, st + 16 * chunk_at<CPR>((lane & 7) + (((lane >> 3) & 1) << 3), ks + (lane >> 4)));
-            }
 #pragma unroll
             for (int x = 0; x < (KV8 ? 2 : 1); ++x) {
-                unsigned b[2][2];
-                if (!KV8) {
-                    b[0][0] = r[0]; b[0][1] = r[1]; b[1][0] = r[2]; b[1][1] = r[3];
-                } else {
+                unsigned f[MT][4];
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
-                        b[nt][0] = unpack_e4m3((unsigned short)r[2 * x + nt]);
-                        b[nt][1] = unpack_e4m3((unsigned short)(r[2 * x + nt] >> 16));
+                for (int mt = 0; mt < MT; ++mt) {
+                    if (S::QREG) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) f[mt][e] = qf[S::QREG ? mt : 0][S::QREG ? ks + x : 0][e];
+                    } else {
+                        const uint4 w = qs[(mt * KS + ks + x) * 32 + lane];
+                        f[mt][0] = w.x; f[mt][1] = w.y; f[mt][2] = w.z; f[mt][3] = w.w;
                     }
                 }
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    unsigned f[4];
-                    if (S::QREG) {
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) f[e] = qf[S::QREG ? mt : 0][S::QREG ? ks + x : 0][e];
+                for (int h = 0; h < H; ++h) {
+                    unsigned b[2][2];
+                    if (!KV8) {
+                        // matrices: tokens 0-7 at k 0-7, k 8-15, tokens 8-15 at k 0-7, k 8-15
+                        unsigned r[4];
+                        ldsm_x4(r, st + h * S::HALF + 16 * chunk_at<CPR>((lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1)));
+                        b[0][0] = r[0]; b[0][1] = r[1]; b[1][0] = r[2]; b[1][1] = r[3];
                     } else {
-                        const uint4 w = qs[(mt * KS + ks + x) * 32 + lane];
-                        f[0] = w.x; f[1] = w.y; f[2] = w.z; f[3] = w.w;
+                        // matrices: tokens 0-7, 8-15 at bytes 16 ks .., then at bytes 16 (ks + 1) ..
+                        if (x == 0) ldsm_x4(kb[h], st + h * S::HALF + 16 * chunk_at<CPR>((lane & 7) + (((lane >> 3) & 1) << 3), ks + (lane >> 4)));
+#pragma unroll
+                        for (int nt = 0; nt < 2; ++nt) {
+                            b[nt][0] = unpack_e4m3((unsigned short)kb[h][2 * x + nt]);
+                            b[nt][1] = unpack_e4m3((unsigned short)(kb[h][2 * x + nt] >> 16));
+                        }
                     }
-                    mma_rows<MB>(s[mt][0], f, b[0][0], b[0][1]);
-                    mma_rows<MB>(s[mt][1], f, b[1][0], b[1][1]);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        mma_rows<MB>(s[mt][2 * h], f[mt], b[0][0], b[0][1]);
+                        mma_rows<MB>(s[mt][2 * h + 1], f[mt], b[1][0], b[1][1]);
+                    }
                 }
             }
         }
-        // ---- exponents of the piece's keys and values (tokens 2 t4, 2 t4 + 1, + 8 of this thread)
-        float vf[2][2];
+        // ---- exponents of the keys and values (tokens 8 nt + 2 t4, + 1 of this thread)
+        float vf[2 * H][2];
         if (KV8) {
-            const unsigned char *ke = st + 2 * S::TILE, *ve = ke + 16;
-            uint4 all = *reinterpret_cast<const uint4 *>(ve);
-            if (j0 + kPiece > u.hi) {  // bytes past the range are not the request's
-                unsigned w[4] = {all.x, all.y, all.z, all.w};
+            const unsigned char *ex = st + 2 * S::TILE;  // of each half: 16 keys', 16 values'
+            unsigned top = 0;
 #pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int livebytes = min(max(u.hi - j0 - 4 * x, 0), 4);
-                    if (livebytes < 4) w[x] &= (1u << (8 * livebytes)) - 1u;
+            for (int h = 0; h < H; ++h) {
+                const uint4 all = *reinterpret_cast<const uint4 *>(ex + 32 * h + 16);
+                unsigned w[4] = {all.x, all.y, all.z, all.w};
+                if (j0 + 16 * h + 16 > u.hi) {  // bytes past the range are not the request's
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int livebytes = min(max(u.hi - j0 - 16 * h - 4 * x, 0), 4);
+                        if (livebytes < 4) w[x] &= (1u << (8 * livebytes)) - 1u;
+                    }
                 }
-                all = make_uint4(w[0], w[1], w[2], w[3]);
+                top = __vmaxu4(top, __vmaxu4(__vmaxu4(w[0], w[1]), __vmaxu4(w[2], w[3])));
             }
-            unsigned top = __vmaxu4(__vmaxu4(all.x, all.y), __vmaxu4(all.z, all.w));
             top = __vmaxu4(top, top >> 16);
             top = max(top & 0xffu, (top >> 8) & 0xffu);
             if ((int)top > ref) {  // the same in every lane
@@ -285,40 +305,42 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a, bool io_bf) {
                         for (int e = 0; e < 4; ++e) o[mt][j][e] *= f;
             }
 #pragma unroll
-            for (int nt = 0; nt < 2; ++nt)
+            for (int nt = 0; nt < 2 * H; ++nt) {
+                const unsigned char *at = ex + 32 * (nt / 2) + 8 * (nt & 1) + 2 * t4;
+                const unsigned k2 = *reinterpret_cast<const unsigned short *>(at), v2 = *reinterpret_cast<const unsigned short *>(at + 16);
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int tok = 8 * nt + 2 * t4 + e;
-                    const float kf = exp_byte(ke[tok]);
-                    const int x = (int)ve[tok] - ref + 15 + 127;
+                    const float kf = exp_byte((k2 >> (8 * e)) & 0xffu);
+                    const int x = (int)((v2 >> (8 * e)) & 0xffu) - ref + 15 + 127;
                     vf[nt][e] = __int_as_float(max(x, 0) << 23);
-                    if (j0 + tok >= u.hi) vf[nt][e] = 0.f;
+                    if (j0 + 8 * nt + 2 * t4 + e >= u.hi) vf[nt][e] = 0.f;
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
                         s[mt][nt][e] *= kf;
                         s[mt][nt][2 + e] *= kf;
                     }
                 }
+            }
         }
         // ---- masks: only pieces that some row does not see in full
-        const bool edge = j0 + kPiece - 1 > row0_pos || j0 + kPiece > u.hi || (a.window && j0 <= last - a.window);
+        const bool edge = j0 + P - 1 > row0_pos || j0 + P > u.hi || (a.window && j0 <= last - a.window);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
             for (int hh = 0; hh < 2; ++hh) {
+                if (edge) {
+#pragma unroll
+                    for (int nt = 0; nt < 2 * H; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int j = j0 + 8 * nt + 2 * t4 + e;
+                            if (j > pos[mt][hh] || j >= u.hi || (a.window && j <= pos[mt][hh] - a.window)) s[mt][nt][2 * hh + e] = -INFINITY;
+                        }
+                }
                 float big = -INFINITY;
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float &x = s[mt][nt][2 * hh + e];
-                        x *= row_scale[mt][hh];
-                        if (edge) {
-                            const int j = j0 + 8 * nt + 2 * t4 + e;
-                            if (j > pos[mt][hh] || j >= u.hi || (a.window && j <= pos[mt][hh] - a.window)) x = -INFINITY;
-                        }
-                        big = fmaxf(big, x);
-                    }
+                for (int nt = 0; nt < 2 * H; ++nt) big = fmaxf(fmaxf(big, s[mt][nt][2 * hh]), s[mt][nt][2 * hh + 1]);
+                big *= row_scale[mt][hh];
                 big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
                 big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
                 const float mn = fmaxf(m[mt][hh], big);
@@ -335,41 +357,44 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a, bool io_bf) {
                     m[mt][hh] = mn;
                 }
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
+                for (int nt = 0; nt < 2 * H; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         float &x = s[mt][nt][2 * hh + e];
-                        x = exp2_fast(x - base);
+                        x = exp2_fast(fmaf(x, row_scale[mt][hh], -base));
                         l[mt][hh] += x;
                         if (KV8) x *= vf[nt][e];
                     }
             }
         // ---- output: p (16 rows x 16 tokens, rounded to 16 bits) times the values
-        unsigned pf[MT][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int h = 0; h < H; ++h) {
+            unsigned pf[MT][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) pf[mt][e] = pack2<MB>(s[mt][e >> 1][2 * (e & 1)], s[mt][e >> 1][2 * (e & 1) + 1]);
-        const unsigned char *sv = st + S::TILE;
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int c = 0; c < CPR; c += 2) {
-            // matrices: tokens 0-7, 8-15 at chunk c, then at chunk c + 1, transposed
-            unsigned r[4];
-            ldsm_x4_t(r, sv + 16 * chunk_at<CPR>((lane & 7) + (((lane >> 3) & 1) << 3), c + (lane >> 4)));
+                for (int e = 0; e < 4; ++e) pf[mt][e] = pack2<MB>(s[mt][2 * h + (e >> 1)][2 * (e & 1)], s[mt][2 * h + (e >> 1)][2 * (e & 1) + 1]);
+            const unsigned char *sv = st + S::TILE + h * S::HALF;
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-                if (!KV8) {
+            for (int c = 0; c < CPR; c += 2) {
+                // matrices: tokens 0-7, 8-15 at chunk c, then at chunk c + 1, transposed
+                unsigned r[4];
+                ldsm_x4_t(r, sv + 16 * chunk_at<CPR>((lane & 7) + (((lane >> 3) & 1) << 3), c + (lane >> 4)));
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) mma_rows<MB>(o[mt][c + x], pf[mt], r[2 * x], r[2 * x + 1]);
-                } else {
-                    // bytes (token, column): (0, 0) (0, 1) (1, 0) (1, 1) -> the even and the odd columns
-                    const unsigned w0 = __byte_perm(r[2 * x], 0, 0x3120), w1 = __byte_perm(r[2 * x + 1], 0, 0x3120);
-                    const unsigned e0 = unpack_e4m3((unsigned short)w0), e1 = unpack_e4m3((unsigned short)w1);
-                    const unsigned d0 = unpack_e4m3((unsigned short)(w0 >> 16)), d1 = unpack_e4m3((unsigned short)(w1 >> 16));
+                for (int x = 0; x < 2; ++x) {
+                    if (!KV8) {
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        mma_rows<MB>(o[mt][2 * (c + x)], pf[mt], e0, e1);
-                        mma_rows<MB>(o[mt][2 * (c + x) + 1], pf[mt], d0, d1);
+                        for (int mt = 0; mt < MT; ++mt) mma_rows<MB>(o[mt][c + x], pf[mt], r[2 * x], r[2 * x + 1]);
+                    } else {
+                        // bytes (token, column): (0, 0) (0, 1) (1, 0) (1, 1) -> the even and the odd columns
+                        const unsigned w0 = __byte_perm(r[2 * x], 0, 0x3120), w1 = __byte_perm(r[2 * x + 1], 0, 0x3120);
+                        const unsigned e0 = unpack_e4m3((unsigned short)w0), e1 = unpack_e4m3((unsigned short)w1);
+                        const unsigned d0 = unpack_e4m3((unsigned short)(w0 >> 16)), d1 = unpack_e4m3((unsigned short)(w1 >> 16));
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            mma_rows<MB>(o[mt][2 * (c + x)], pf[mt], e0, e1);
+                            mma_rows<MB>(o[mt][2 * (c + x) + 1], pf[mt], d0, d1);
+                        }
                     }
                 }
             }
@@ -536,7 +561,7 @@ AttnPlan attn_plan(int B, int total, int G, int D) {
     const long long rows = B > 0 ? ((long long)total * G + B - 1) / B : 0;
     if (rows > (D == 256 ? 16 : 32) && G <= 128)
         return {true, 128 / G * G * (D == 256 ? 1 : 2), kAttnSms, D == 256 ? 64 : 128, 512};
-    return {false, rows <= 16 ? 16 : 32, 4 * kAttnSms, 64, 256};
+    return {false, rows <= 16 ? 16 : 32, 8 * kAttnSms, 128, 256};
 }
 
 template <int D, int MT, bool BF, bool KV8>
@@ -601,8 +626,10 @@ extern "C" dn_status dn_attn_paged(int B, int total, int heads_kv, int group, in
         workspace_bytes < dn_attn_workspace_bytes(B, total, heads_kv, group, D))
         return DN_ERR_INVALID_ARG;
     AttnPlan p = attn_plan(B, total, group, D);
-    if (pages == 0 || max_pages == 0) p = {false, 16, kAttnSms, 64, 256};  // nothing is cached: no pool to copy from
-    const long long units = attn_units_bound(B, total, heads_kv, group, p.M, p.target);
+    if (pages == 0 || max_pages == 0) p = {false, 16, kAttnSms, 128, 256};  // nothing is cached: no pool to copy from
+    // at most this many units; a table of few pages bounds the ranges of a tile as well
+    const long long units = std::min(attn_units_bound(B, total, heads_kv, group, p.M, p.target),
+                                     attn_tiles_bound(B, total, group, p.M) * heads_kv * std::max(1LL, ((long long)max_pages * page + p.min_range - 1) / p.min_range));
     if (units > 0x7fffffffLL) return DN_ERR_INVALID_ARG;
     AttnArgs a;
     a.p = {start, kv_len, page_table, B, total, max_pages, pages, page_log2(page), heads_kv};
