@@ -553,15 +553,19 @@ attn_join_kernel(const __grid_constant__ AttnArgs a, bool bf) {
 
 struct AttnPlan {
     bool tc;
-    int M, target, align, min_range;
+    int M, wave, target, align, min_range;
 };
 
-AttnPlan attn_plan(int B, int total, int G, int D) {
+AttnPlan attn_plan(int B, int total, int G, int D, bool kv8) {
     // rows of a request, on average over the batch
     const long long rows = B > 0 ? ((long long)total * G + B - 1) / B : 0;
-    if (rows > (D == 256 ? 16 : 32) && G <= 128)
-        return {true, 128 / G * G * (D == 256 ? 1 : 2), kAttnSms, D == 256 ? 64 : 128, 512};
-    return {false, rows <= 16 ? 16 : 32, 8 * kAttnSms, 128, 256};
+    // Warp MMAs up to 16 rows, and up to 32 where tcgen05 tiles are no faster: 64 requests x 8,000 tokens, 24 rows of
+    // each of 4 key heads: D = 128 in 16 bits 218 us on warps and 201 in tiles, in 8 bits 198 and 349, D = 64 128 and 163.
+    // D = 256 holds 16 rows a warp.
+    if (rows > (D == 256 || (D == 128 && !kv8) ? 16 : 32) && G <= 128)
+        return {true, 128 / G * G * (D == 256 ? 1 : 2), kAttnSms, kAttnSms, D == 256 ? 64 : 128, 512};
+    const int resident = D == 256 ? (kv8 ? 2 : 1) : 3;  // CTAs an SM
+    return {false, rows <= 16 ? 16 : 32, resident * kAttnSms, 8 * kAttnSms, 64, 64};
 }
 
 template <int D, int MT, bool BF, bool KV8>
@@ -574,8 +578,10 @@ void launch_rows(const AttnArgs &a, bool io_bf, unsigned grid, cudaStream_t st) 
 template <int D, int MT>
 void launch_rows(const AttnArgs &a, bool bf, bool kv8, unsigned grid, cudaStream_t st) {
     if (kv8) launch_rows<D, MT, false, true>(a, bf, grid, st);
-    else if (bf) launch_rows<D, MT, true, false>(a, bf, grid, st);
-    else launch_rows<D, MT, false, false>(a, bf, grid, st);
+    else if constexpr (D == 64 || MT == 1) {
+        if (bf) launch_rows<D, MT, true, false>(a, bf, grid, st);
+        else launch_rows<D, MT, false, false>(a, bf, grid, st);
+    }
 }
 
 }  // namespace
@@ -591,8 +597,8 @@ void launch_join(const AttnArgs &a, int D, bool bf, unsigned pairs, unsigned row
 // Few tiles have many ranges each: a CTA a row, as long as that is at most a few waves of CTAs. Many tiles
 // have few ranges, and most CTAs of a grid that covers them all have nothing to join: eight rows a CTA.
 void launch_attn_join(const AttnArgs &a, int D, bool bf, cudaStream_t st) {
-    const long long pairs = min((long long)a.target, attn_tiles_bound(a.p.B, a.p.total, a.G, a.M) * a.p.heads);
-    const long long rows = min((long long)a.M, (long long)a.p.total * a.G);
+    const long long pairs = std::min((long long)std::max(a.target, a.wave), attn_tiles_bound(a.p.B, a.p.total, a.G, a.M) * a.p.heads);
+    const long long rows = std::min((long long)a.M, (long long)a.p.total * a.G);
     if (pairs * rows <= 8 * kAttnSms) launch_join<1>(a, D, bf, (unsigned)pairs, (unsigned)rows, st);
     else launch_join<8>(a, D, bf, (unsigned)pairs, (unsigned)rows, st);
 }
@@ -602,8 +608,12 @@ void launch_attn_join(const AttnArgs &a, int D, bool bf, cudaStream_t st) {
 extern "C" size_t dn_attn_workspace_bytes(int B, int total, int heads_kv, int group, int D) {
     using namespace dn;
     if (B < 1 || total < 1 || total > DN_KV_MAX_ROWS || heads_kv < 1 || group < 1 || !kv_shape_ok(D, 16)) return 0;
-    const AttnPlan p = attn_plan(B, total, group, D);
-    return (size_t)2 * p.target * p.M * (D + 2) * sizeof(float);
+    size_t most = 0;
+    for (int kv8 = 0; kv8 < 2; ++kv8) {
+        const AttnPlan p = attn_plan(B, total, group, D, kv8);
+        most = std::max(most, (size_t)2 * std::max(p.target, p.wave) * p.M * (D + 2) * sizeof(float));
+    }
+    return most;
 }
 
 extern "C" dn_status dn_attn_paged(int B, int total, int heads_kv, int group, int D, int page, int max_pages, int pages,
@@ -625,11 +635,14 @@ extern "C" dn_status dn_attn_paged(int B, int total, int heads_kv, int group, in
         !out || !workspace || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16) ||
         workspace_bytes < dn_attn_workspace_bytes(B, total, heads_kv, group, D))
         return DN_ERR_INVALID_ARG;
-    AttnPlan p = attn_plan(B, total, group, D);
-    if (pages == 0 || max_pages == 0) p = {false, 16, kAttnSms, 128, 256};  // nothing is cached: no pool to copy from
-    // at most this many units; a table of few pages bounds the ranges of a tile as well
-    const long long units = std::min(attn_units_bound(B, total, heads_kv, group, p.M, p.target),
-                                     attn_tiles_bound(B, total, group, p.M) * heads_kv * std::max(1LL, ((long long)max_pages * page + p.min_range - 1) / p.min_range));
+    AttnPlan p = attn_plan(B, total, group, D, cache_dt == DN_E4M3);
+    if (pages == 0 || max_pages == 0) p = {false, 16, kAttnSms, kAttnSms, 64, 64};  // nothing is cached: no pool to copy from
+    // At most this many units: few tiles are cut for one wave (CTAs without a unit cost their launch, 5 us for
+    // 1,000 of the largest), and a table of few pages bounds the ranges of a tile.
+    const long long whole = attn_tiles_bound(B, total, group, p.M) * heads_kv;
+    if (2 * whole < p.wave) p.target = p.wave;
+    const long long units = std::min(std::max(p.target, p.wave) + whole,
+                                     whole * std::max(1LL, ((long long)max_pages * page + p.min_range - 1) / p.min_range));
     if (units > 0x7fffffffLL) return DN_ERR_INVALID_ARG;
     AttnArgs a;
     a.p = {start, kv_len, page_table, B, total, max_pages, pages, page_log2(page), heads_kv};
@@ -647,6 +660,7 @@ extern "C" dn_status dn_attn_paged(int B, int total, int heads_kv, int group, in
     a.window = window >= DN_KV_MAX_TOKENS ? 0 : window;
     a.M = p.M;
     a.align = p.align;
+    a.wave = p.wave;
     a.target = p.target;
     a.min_range = p.min_range;
     const bool bf = io_dt == DN_BF16, kv8 = cache_dt == DN_E4M3;
@@ -659,6 +673,6 @@ extern "C" dn_status dn_attn_paged(int B, int total, int heads_kv, int group, in
     else if (D == 128 && p.M == 16) launch_rows<128, 1>(a, bf, kv8, (unsigned)units, st);
     else if (D == 128) launch_rows<128, 2>(a, bf, kv8, (unsigned)units, st);
     else launch_rows<256, 1>(a, bf, kv8, (unsigned)units, st);
-    launch_attn_join(a, D, bf, st);
+    if (units > whole) launch_attn_join(a, D, bf, st);  // (else no tile can have two ranges)
     return launch_status();
 }

@@ -6,15 +6,17 @@
 //
 // Units. A unit is a tile, a key head and a range of cached tokens, the work of one CTA. Lengths are
 // known on the device only, so every CTA finds its own unit: its warps read the B requests' lengths,
-// sum the work (tiles x tokens x heads), take the range length C that makes about `target` units of it,
-// and look their unit up in the running count. A long cache with few rows is cut into many ranges, a
-// request shorter than C is one unit, and the batch is even whatever its lengths. The host sizes the
-// grid by a bound (units_bound); CTAs past the last unit leave.
+// sum the work (tiles x tokens x heads), take the range length C that makes so many units of it, and look
+// their unit up in the running count. If there are fewer tiles than half the CTAs that run at once, that
+// is one wave of equal ranges (a single request's long cache: D = 256, one token over 25,000, took 27.7 us so
+// and 39.5 in four waves); else it is a few waves, whose ends even out requests of all lengths (64
+// requests: 173 us against 191 in one wave). A request's ranges are of one length. The host sizes the grid
+// by a bound; CTAs past the last unit leave.
 //
 // Partials. A tile seen in one range is finished by its unit. Otherwise every range leaves the running
 // maximum, the sum and the unnormalised output of its rows (32 bits) in a slot of the workspace,
 // and attn_join_kernel adds them in the order of the ranges, so results repeat bit for bit. Only
-// requests with at least two ranges own slots, and those have fewer than 2 * target of them
+// requests with at least two ranges own slots, and those have fewer than 2 * max(target, wave) of them
 // (a request of span > C has fewer than 2 span / C ranges), whatever B and the lengths are.
 #pragma once
 
@@ -39,8 +41,9 @@ struct AttnArgs {
     float scale_log2;  // scale * log2(e): scores are kept in powers of two
     int window;        // 0: none
     int M;             // rows of a tile
-    int align;         // ranges start at multiples of this many tokens
-    int target, min_range;
+    int align;         // ranges start at multiples of this many tokens (a power of two)
+    int wave, target;  // units: CTAs that run at once, and of a batch (at least as many)
+    int min_range;
 };
 
 struct AttnUnit {
@@ -55,10 +58,6 @@ __host__ __device__ inline long long attn_tiles_bound(int B, int total, int G, i
     const long long rows = (long long)total * G;
     return rows / M + (B < total ? B : total);
 }
-__host__ __device__ inline long long attn_units_bound(int B, int total, int heads, int G, int M, int target) {
-    return target + attn_tiles_bound(B, total, G, M) * heads;
-}
-
 // A request's packed rows, cached tokens, tiles and the most tokens that one of its tiles sees.
 __device__ __forceinline__ void attn_request(const AttnArgs &a, int b, int &s, int &n, int &first, int &len, int &tiles,
                                              int &span) {
@@ -76,22 +75,31 @@ template <bool JOIN>
 __device__ __forceinline__ bool attn_unit(const AttnArgs &a, int idx, AttnUnit &u) {
     const int lane = threadIdx.x % 32, B = a.p.B;
     long long work = 0;
+    int whole = 0;  // tiles
+    int s = 0, n = 0, first = 0, len = 0, tiles = 0, span = 0;
     for (int i = 0; i < B; i += 32) {
-        int s, n, first, len, tiles = 0, span = 0;
+        tiles = span = 0;
         if (i + lane < B) attn_request(a, i + lane, s, n, first, len, tiles, span);
         work += (long long)tiles * span;
+        whole += tiles;
     }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) work += __shfl_xor_sync(0xffffffffu, work, off);
+    whole = __reduce_add_sync(0xffffffffu, whole);
+    const int target = 2 * (long long)whole * a.p.heads < a.wave ? a.wave : a.target;
     // C = work * heads / target, rounded up to a multiple of align: in 32 bits unless the work is huge
-    work = work * a.p.heads + a.target - 1;
-    const long long C = work < 0x7fffffff ? (int)work / a.target : work / a.target;
-    const int range = max((int)min((C + a.align - 1) / a.align * a.align, 1ll << 30), a.min_range);
+    work = work * a.p.heads + target - 1;
+    const long long C = work < 0x7fffffff ? (int)work / target : work / target;
+    const int most = max((int)min((C + a.align - 1) & ~(long long)(a.align - 1), 1ll << 30), a.min_range);
     int before = 0, slots_before = 0;
     for (int i = 0; i < B; i += 32) {
-        int s = 0, n = 0, first = 0, len = 0, tiles = 0, span = 0;
-        if (i + lane < B) attn_request(a, i + lane, s, n, first, len, tiles, span);
-        const int ranges = max(1, (span + range - 1) / range);  // (both at most 2^30)
+        if (B > 32) {  // (else the values of the loop above)
+            tiles = span = 0;
+            if (i + lane < B) attn_request(a, i + lane, s, n, first, len, tiles, span);
+        }
+        // equal ranges of at most `most` tokens (all at most 2^30)
+        const int cut = max(1, (span + most - 1) / most), range = max(a.min_range, ((span + cut - 1) / cut + a.align - 1) & ~(a.align - 1));
+        const int ranges = max(1, (span + range - 1) / range);
         const int slots = ranges > 1 ? tiles * ranges * a.p.heads : 0;
         const int units = JOIN ? (ranges > 1 ? tiles * a.p.heads : 0) : tiles * ranges * a.p.heads;
         int upto = units, slots_upto = slots;
@@ -112,7 +120,7 @@ __device__ __forceinline__ bool attn_unit(const AttnArgs &a, int idx, AttnUnit &
             u.n = from(n);
             u.first = from(first);
             u.len = from(len);
-            const int T = from(tiles), R = from(ranges);
+            const int T = from(tiles), R = from(ranges), step = from(range);
             int local = idx - before - from(upto - units);
             // neighbours in the grid are tiles of one range, so they share its pages in L2; the
             // last tile of a prompt, which sees most, comes first
@@ -125,9 +133,9 @@ __device__ __forceinline__ bool attn_unit(const AttnArgs &a, int idx, AttnUnit &
             const int hi = min(max(u.first + r1 / a.G + 1, 0), u.len);
             int lo = a.window ? max(u.first + r0 / a.G - a.window + 1, 0) : 0;
             lo = min(lo & ~(a.align - 1), hi);  // (align is a power of two)
-            u.ranges = max(1, (hi - lo + range - 1) / range);
-            u.lo = u.c < u.ranges ? lo + u.c * range : hi;
-            u.hi = hi - u.lo > range ? u.lo + range : hi;
+            u.ranges = max(1, (hi - lo + step - 1) / step);
+            u.lo = u.c < u.ranges ? lo + u.c * step : hi;
+            u.hi = hi - u.lo > step ? u.lo + step : hi;
             return true;
         }
         before += __shfl_sync(0xffffffffu, upto, 31);

@@ -147,7 +147,7 @@ struct TileShape {
     static constexpr int HALVES = D / 64;            // 64-column boxes of a tile
     static constexpr int TILE = BN * D * 2;          // bytes of a 16-bit K or V tile
     static constexpr int QTILE = 128 * D * 2;
-    static constexpr int SLOTS = KV8 ? (D == 64 ? 4 : 3) : (D == 64 ? 8 : 5);
+    static constexpr int SLOTS = KV8 ? (D == 64 ? 4 : 3) : (D == 64 ? 6 : 5);
     static constexpr int RAW = KV8 ? BN * D : 0;     // bytes of an 8-bit tile
     static constexpr int RAWS = KV8 ? (D == 64 ? 4 : 3) : 0;
     static constexpr int SOFTMAX = 128 * NS;         // threads of the softmax warpgroups
@@ -162,14 +162,18 @@ struct TileShape {
     static constexpr int OFF_RAW = OFF_RING + SLOTS * TILE;
     // [RAWS][2][8][128]: exponent bytes of a tile's keys and values (values alone with the values), 128 bytes (a copy's alignment) a page
     static constexpr int OFF_EXP = OFF_RAW + RAWS * RAW;
-    static constexpr int OFF_BAR = OFF_EXP + RAWS * 2048;
+    static constexpr int OFF_POW = OFF_EXP + RAWS * 2048;  // [warps][BN] powers of two of a tile's tokens
+    static constexpr int OFF_BAR = OFF_POW + 2 * CVT / 32 * BN * 4;
     static constexpr int BYTES = OFF_BAR + 1024 + 1024;                        // and the alignment of the base
     static_assert(BYTES <= 232448, "shared memory of one CTA");
+    // Barriers go by tile modulo 4, so a tile's copy must not be issued before the tile four earlier has been
+    // used: key tile 4 is the eighth copy of a ring (see seq_k), tile 0 the first.
+    static_assert(SLOTS <= 7 && RAWS <= 7, "a ring holds fewer copies than lie between tiles t and t + 4");
     static_assert(NS == 1 || 8192 + 128 * (D + 4) * 4 + 1024 <= SLOTS * TILE, "the streams merge in the ring");
 };
 
 struct Bars {
-    // by kind (keys, values) and tile modulo 4: a ring is at most eight slots, so four tiles, ahead
+    // by kind (keys, values) and tile modulo 4
     unsigned long long full[2][4], empty[2][4], raw_full[2][4], raw_empty[2][4], ref_full[4], s_full[2], p_full[2], pv, q_full, q_ready, last_v, fin;
     uint32_t tmem;
     int abort, k_ref[4], v_ref[4];
@@ -404,30 +408,51 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                 bar.v_ref[t & 3] = ref_most;
                 mbar_arrive(&bar.ref_full[t & 3]);
             }
+            // 2^(E - R) of each token in fp16, twice (subnormal below 2^-14, zero below 2^-24), a copy in every warp
+            unsigned *mine = reinterpret_cast<unsigned *>(smem + S::OFF_POW) + (warp - W_TMA - 2) * BN;
+            if (4 * lane < BN) {
+                unsigned f[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int E = (int)((e4 >> (8 * e)) & 0xffu) - R;
+                    f[e] = (E >= -14 ? (unsigned)(15 + E) << 10 : E >= -24 ? 1u << (24 + E) : 0u) * 0x10001u;
+                }
+                *reinterpret_cast<uint4 *>(mine + 4 * lane) = make_uint4(f[0], f[1], f[2], f[3]);
+            }
+            __syncwarp();
             const unsigned char *src = raw + rs * S::RAW;
             unsigned char *dst = ring + slot * TILE;
-            constexpr int CHUNKS = BN * D / 16, PER = KV8 ? (CHUNKS + S::CVT - 1) / (KV8 ? S::CVT : 1) : 1;
+            constexpr int CHUNKS = BN * D / 16, PER = KV8 ? (CHUNKS + S::CVT - 1) / (KV8 ? S::CVT : 1) : 1, BATCH = 4;
 #pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int x = i * S::CVT + c, r = x / (D / 16), e = x % (D / 16) * 16, half = e / 64, ch = e % 64 / 8;
-                // 2^(E - R) in fp16: subnormal below 2^-14, zero below 2^-24; rows past the range are zeros
-                const int E = (int)((__shfl_sync(0xffffffffu, e4, (r / 4) & 31) >> (8 * (r & 3))) & 0xffu) - R;
-                const __half2 f = __float2half2_rn(__int_as_float(max(E + 127, 0) << 23));
-                if (x >= CHUNKS) break;  // (a warp's 32 chunks at once)
-                uint4 w = *reinterpret_cast<const uint4 *>(src + x * 16);
-                if (r >= live) w = make_uint4(0, 0, 0, 0);
-                auto two = [&](unsigned v) {
-                    const unsigned h = unpack_e4m3((unsigned short)v);
-                    const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&h), f);
-                    return *reinterpret_cast<const unsigned *>(&y);
-                };
-                uint4 o[2];
-                o[0] = make_uint4(two(w.x), two(w.x >> 16), two(w.y), two(w.y >> 16));
-                o[1] = make_uint4(two(w.z), two(w.z >> 16), two(w.w), two(w.w >> 16));
-                unsigned char *row = dst + half * BN * 128 + r * 128;
-                const int first = half & 1;  // lanes of neighbouring halves store to different banks
-                *reinterpret_cast<uint4 *>(row + (((ch + first) ^ (r & 7)) << 4)) = first ? o[1] : o[0];
-                *reinterpret_cast<uint4 *>(row + (((ch + 1 - first) ^ (r & 7)) << 4)) = first ? o[0] : o[1];
+            for (int i0 = 0; i0 < PER; i0 += BATCH) {
+                uint4 w[BATCH];
+                unsigned f[BATCH];
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) {
+                    const int x = (i0 + i) * S::CVT + c, r = x / (D / 16);
+                    w[i] = make_uint4(0, 0, 0, 0);
+                    if (i0 + i < PER && x < CHUNKS) {  // (a warp's 32 chunks at once)
+                        f[i] = mine[r];
+                        if (r < live) w[i] = *reinterpret_cast<const uint4 *>(src + x * 16);  // rows past the range are zeros
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < BATCH; ++i) {
+                    const int x = (i0 + i) * S::CVT + c, r = x / (D / 16), e = x % (D / 16) * 16, half = e / 64, ch = e % 64 / 8;
+                    if (i0 + i >= PER || x >= CHUNKS) break;
+                    auto two = [&](unsigned v) {
+                        const unsigned h = unpack_e4m3((unsigned short)v);
+                        const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&f[i]));
+                        return *reinterpret_cast<const unsigned *>(&y);
+                    };
+                    uint4 o[2];
+                    o[0] = make_uint4(two(w[i].x), two(w[i].x >> 16), two(w[i].y), two(w[i].y >> 16));
+                    o[1] = make_uint4(two(w[i].z), two(w[i].z >> 16), two(w[i].w), two(w[i].w >> 16));
+                    unsigned char *row = dst + half * BN * 128 + r * 128;
+                    const int first = half & 1;  // lanes of neighbouring halves store to different banks
+                    *reinterpret_cast<uint4 *>(row + (((ch + first) ^ (r & 7)) << 4)) = first ? o[1] : o[0];
+                    *reinterpret_cast<uint4 *>(row + (((ch + 1 - first) ^ (r & 7)) << 4)) = first ? o[0] : o[1];
+                }
             }
             fence_proxy_async();
             mbar_arrive(&bar.full[is_v][t & 3]);
