@@ -15,7 +15,7 @@
 //
 // Copies. K and V tiles pass through one ring of shared-memory slots in the order in which the products take
 // them. Pages come in by TMA, one box per page and 64 columns, with the 128-byte swizzle that the MMA
-// descriptors read; each lane of the producer warp looks up and copies a box of its own. A page that a
+// descriptors read; the producer's lanes look the pages up 32 at a time. A page that a
 // request does not have is an out-of-range coordinate, which the copy fills with zeros. Rows of the last
 // page past the range may hold anything: their scores are masked, and their values are zeroed in
 // shared memory before the product (0 x NaN is not 0). q comes the same way, G heads by 128 / G tokens a
@@ -107,11 +107,6 @@ __device__ __forceinline__ void tma_load_3d(void *smem, const void *tmap, int c0
                  " [%0], [%1, {%2, %3, %4}], [%5];"
                  :: "r"(smem_addr(smem)), "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(mb)) : "memory");
 }
-__device__ __forceinline__ void tma_load_2d(void *smem, const void *tmap, int c0, int c1, unsigned long long *mb) {
-    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                 " [%0], [%1, {%2, %3}], [%4];"
-                 :: "r"(smem_addr(smem)), "l"(tmap), "r"(c0), "r"(c1), "r"(smem_addr(mb)) : "memory");
-}
 __device__ __forceinline__ void mbar_arrive(unsigned long long *mb) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" :: "r"(smem_addr(mb)) : "memory");
 }
@@ -151,30 +146,39 @@ struct TileShape {
     static constexpr int RAW = KV8 ? BN * D : 0;     // bytes of an 8-bit tile
     static constexpr int RAWS = KV8 ? (D == 64 ? 4 : 3) : 0;
     static constexpr int SOFTMAX = 128 * NS;         // threads of the softmax warpgroups
-    // threads that turn 8-bit tiles into fp16, half of them the keys and half the values (so that one's waits
-    // pass beside the other's work): two warps beside the producer's and the products' warp, and the rest
-    static constexpr int CVT = KV8 ? (D == 256 ? 160 : 96) : 0;
-    static constexpr int THREADS = SOFTMAX + 128 + (KV8 ? 2 * CVT - 64 : 0);
+    // Threads that turn 8-bit tiles into fp16: one group for the keys and one for the values, so that one's
+    // waits pass beside the other's work. The more elements a token has, the more of the block's registers
+    // they are worth: for D = 64 the softmax keeps its scores in registers (three prompts' window of 1,000 took
+    // 88 us so, and 104 with 14 such warps), for D = 128 it reads them twice (32 verify blocks of 64 rows: 256 us
+    // with 14 warps, 328 with 6).
+    static constexpr int CVT = KV8 ? (D == 64 ? 64 : D == 128 ? 192 : 256) : 0;
+    static constexpr bool TWICE = KV8 && D == 128;
+    static constexpr int THREADS = SOFTMAX + 128 + 2 * CVT;
+    static_assert(THREADS % 128 == 0, "register splits go by warpgroups");
     // columns of tensor memory: S at 0 and BN, P in the place of S for D = 128 (where that fills the
     // 512 columns), else beside it
     static constexpr int COL_P = D == 128 ? 0 : D == 64 ? 384 : 128, P_STEP = D == 128 ? BN : BN / 2, COL_O = 256, O_STEP = D;
+    // registers of a softmax thread and of the others; the sum stays within the launch's
+    static constexpr bool SPLIT = NS == 2 || KV8;
+    static constexpr int R_SOFTMAX = !KV8 ? 208 : D == 64 ? 176 : 112, R_OTHER = !KV8 ? 88 : D == 64 ? 80 : D == 128 ? 64 : 72;
+    static constexpr int R_LAUNCH = 65536 / THREADS / 8 * 8;
+    static_assert(!SPLIT || SOFTMAX * R_SOFTMAX + (THREADS - SOFTMAX) * R_OTHER <= THREADS * R_LAUNCH, "registers");
     static constexpr int OFF_RING = NS * QTILE;
     static constexpr int OFF_RAW = OFF_RING + SLOTS * TILE;
-    // [RAWS][2][8][128]: exponent bytes of a tile's keys and values (values alone with the values), 128 bytes (a copy's alignment) a page
-    static constexpr int OFF_EXP = OFF_RAW + RAWS * RAW;
-    static constexpr int OFF_POW = OFF_EXP + RAWS * 2048;  // [warps][BN] powers of two of a tile's tokens
-    static constexpr int OFF_BAR = OFF_POW + 2 * CVT / 32 * BN * 4;
+    static constexpr int OFF_POW = OFF_RAW + RAWS * RAW;  // [2][4][BN]: powers of two of a key or value tile's tokens
+    static constexpr int OFF_BAR = OFF_POW + (KV8 ? 2 * 4 * BN * 4 : 0);
     static constexpr int BYTES = OFF_BAR + 1024 + 1024;                        // and the alignment of the base
     static_assert(BYTES <= 232448, "shared memory of one CTA");
     // Barriers go by tile modulo 4, so a tile's copy must not be issued before the tile four earlier has been
     // used: key tile 4 is the eighth copy of a ring (see seq_k), tile 0 the first.
-    static_assert(SLOTS <= 7 && RAWS <= 7, "a ring holds fewer copies than lie between tiles t and t + 4");
+    static_assert(SLOTS + (NS == 2) <= 7 && RAWS <= 7, "a ring holds fewer copies than lie between tiles t and t + 4");
+    static_assert(NS == 1 || QTILE == TILE, "a q tile's place is a slot");
     static_assert(NS == 1 || 8192 + 128 * (D + 4) * 4 + 1024 <= SLOTS * TILE, "the streams merge in the ring");
 };
 
 struct Bars {
     // by kind (keys, values) and tile modulo 4
-    unsigned long long full[2][4], empty[2][4], raw_full[2][4], raw_empty[2][4], ref_full[4], s_full[2], p_full[2], pv, q_full, q_ready, last_v, fin;
+    unsigned long long full[2][4], empty[2][4], raw_full[2][4], raw_empty[2][4], pow_full[2][4], ref_full[4], s_full[2], p_full[2], pv, q_full, q_ready, last_v, fin;
     uint32_t tmem;
     int abort, k_ref[4], v_ref[4];
     signed char q_exp[256];  // powers of two of bf16 q rows brought to fp16
@@ -197,15 +201,14 @@ __device__ __forceinline__ void seq_tile(bool two_q, int seq, int n, int &t, boo
 template <int D, bool BF, bool KV8>
 __global__ void __launch_bounds__(TileShape<D, KV8>::THREADS, 1)
 attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap mq,
-                 const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv,
-                 const __grid_constant__ CUtensorMap mke, const __grid_constant__ CUtensorMap mve, bool io_bf) {
+                 const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, bool io_bf) {
     using S = TileShape<D, KV8>;
     constexpr int BN = S::BN, NS = S::NS, SLOTS = S::SLOTS, TILE = S::TILE;
     constexpr bool MB = BF && !KV8;
     constexpr int W_TMA = S::SOFTMAX / 32, W_MMA = W_TMA + 1;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
-    unsigned char *ring = smem + S::OFF_RING, *raw = smem + S::OFF_RAW, *exps = smem + S::OFF_EXP;
+    unsigned char *raw = smem + S::OFF_RAW;
     Bars &bar = *reinterpret_cast<Bars *>(smem + S::OFF_BAR);
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     if (tid == 0) {
@@ -214,6 +217,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             mbar_init(&bar.empty[i >> 2][i & 3], 1);
             mbar_init(&bar.raw_full[i >> 2][i & 3], 1);
             mbar_init(&bar.raw_empty[i >> 2][i & 3], KV8 ? S::CVT : 1);
+            mbar_init(&bar.pow_full[i >> 2][i & 3], 1);
         }
         for (int i = 0; i < 4; ++i) mbar_init(&bar.ref_full[i], 1);
         for (int i = 0; i < 2; ++i) {
@@ -239,6 +243,11 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
     const bool two_q = NS == 2 && rows > mq_rows;
     const int tiles = (u.hi - u.lo + BN - 1) / BN;
     const int steps = two_q ? 2 * tiles : tiles;
+    // the ring; without a second q tile, its place is one more slot
+    const bool wide = NS == 2 && !two_q;
+    unsigned char *ring = smem + S::OFF_RING - (wide ? S::QTILE : 0);
+    const int slots = wide ? SLOTS + 1 : SLOTS;
+    auto slot_of = [&](int seq) { return wide ? seq % (SLOTS + 1) : seq % SLOTS; };
 
     if (warp == W_MMA) tmem_alloc<512>(&bar.tmem);
     tc_fence_before();
@@ -247,14 +256,15 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
     const uint32_t tm = bar.tmem;
     volatile int *abort = &bar.abort;
 
-    if (warp == W_TMA) {
-        if (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        // ---- producer: a lane per box
-        const int page = 1 << a.p.page_shift, R = min(page, BN), H2 = KV8 ? 1 : S::HALVES;
-        const int boxes = BN / R * H2, sub = lane / H2, half = lane % H2;
-        constexpr int NB = KV8 ? S::RAWS : SLOTS;
+    if (warp == W_TMA || (!KV8 && warp == W_TMA + 3)) {
+        if (S::SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::R_OTHER));
+        // ---- producers. Issuing a copy takes a thread over 100 cycles, so keys and values have a warp each; for 8 bits,
+        // whose boxes are whole rows, one warp does for both.
+        const bool values = warp != W_TMA;
+        const int page = 1 << a.p.page_shift, R = min(page, BN);  // tokens of a box
+        const int NB = KV8 ? S::RAWS : slots;
         int issued = 0;
-        if (tiles > 0 && lane == 0) {
+        if (tiles > 0 && !values && elect_one()) {
             const int tokens = 128 / a.G, boxes_q = S::HALVES * (two_q ? 2 : 1);
             mbar_arrive_expect_tx(&bar.q_full, boxes_q * mq_rows * 128);
             for (int i = 0; i < boxes_q; ++i)
@@ -262,9 +272,9 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                             u.s + row0 / a.G + i / S::HALVES * tokens, &bar.q_full);
         }
         __syncwarp();
-        // pool pages of this unit, 32 boxes' worth a batch, a lane each: the batch that values are taken from
-        // and the next, which keys may be ahead in
-        const int per = BN / R, batch = 32 / per;  // boxes of a tile, tiles of a batch (4 to 32)
+        // pool pages of this unit, 32 boxes' worth a batch, a lane each: the batch in use and the next, which the
+        // keys may be ahead in
+        const int per_log2 = (BN == 128 ? 7 : 6) - min(a.p.page_shift, BN == 128 ? 7 : 6), per = 1 << per_log2;  // boxes of a tile
         auto look = [&](int x) {
             const int j = u.lo + (32 * x + lane) * R, pg = j < u.hi ? pool_page(a.p, u.b, j) : -1;
             return pg < 0 ? a.p.pages : pg;  // past the last page: zeros
@@ -274,13 +284,14 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             int t;
             bool is_v;
             seq_tile(two_q, seq, tiles, t, is_v);
-            const int x = t / batch;
-            if (is_v && x > 0 && t % batch == 0) {
+            if (!KV8 && is_v != values) continue;
+            const int x = (t << per_log2) >> 5;
+            if ((!KV8 || is_v) && x > 0 && ((t << per_log2) & 31) == 0) {
                 if (x & 1) pages_even = look(x + 1);
                 else pages_odd = look(x + 1);
             }
-            const int pg = __shfl_sync(0xffffffffu, x & 1 ? pages_odd : pages_even, (t * per + sub) & 31);
-            const int slot = seq % NB, j0 = u.lo + t * BN;
+            const int ids = x & 1 ? pages_odd : pages_even;
+            const int slot = KV8 ? seq % (KV8 ? S::RAWS : 1) : slot_of(seq), j0 = u.lo + t * BN;
             unsigned long long *full = KV8 ? &bar.raw_full[is_v][t & 3] : is_v && t == tiles - 1 ? &bar.last_v : &bar.full[is_v][t & 3];
             if (seq >= NB) {  // what was in the slot before
                 int t0;
@@ -288,32 +299,33 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                 seq_tile(two_q, seq - NB, tiles, t0, v0);
                 if (!wait_for(KV8 ? &bar.raw_empty[v0][t0 & 3] : &bar.empty[v0][t0 & 3], (t0 >> 2) & 1, abort)) break;
             }
-            if (lane == 0) mbar_arrive_expect_tx(full, KV8 ? S::RAW + (is_v ? BN : 2 * BN) : TILE);
-            __syncwarp();
-            if (lane < boxes) {
-                unsigned char *dst = KV8 ? raw + slot * S::RAW + sub * R * D : ring + slot * TILE + half * BN * 128 + sub * R * 128;
-                const int y = u.h * page + ((j0 + sub * R) & (page - 1));
-                tma_load_3d(dst, is_v ? &mv : &mk, half * 64, y, pg, full);
-                if (KV8) {
-                    if (!is_v) tma_load_2d(exps + slot * 2048 + sub * 128, &mke, y, pg, full);
-                    tma_load_2d(exps + slot * 2048 + 1024 + sub * 128, &mve, y, pg, full);
+            if (elect_one()) mbar_arrive_expect_tx(full, KV8 ? S::RAW : TILE);
+            const int y0 = u.h * page + (j0 & (page - 1));  // (a tile starts a page, or lies in one)
+            for (int box = 0; box < per; ++box) {
+                const int pg = __shfl_sync(0xffffffffu, ids, ((t << per_log2) + box) & 31);
+                if (elect_one()) {
+                    unsigned char *dst = KV8 ? raw + slot * S::RAW + box * R * D : ring + slot * TILE + box * R * 128;
+#pragma unroll
+                    for (int half = 0; half < (KV8 ? 1 : S::HALVES); ++half)
+                        tma_load_3d(dst + half * BN * 128, is_v ? &mv : &mk, half * 64, y0, pg, full);
                 }
             }
+            __syncwarp();
             issued = seq + 1;
         }
         if (*abort) {  // what was copied has to land before the CTA leaves
-            if (tiles > 0) mbar_drain(&bar.q_full, 0);
-            for (int seq = max(0, issued - NB); seq < issued; ++seq)
-            {
+            if (tiles > 0 && !values) mbar_drain(&bar.q_full, 0);
+            for (int seq = max(0, issued - 2 * NB); seq < issued; ++seq) {
                 int t;
                 bool is_v;
                 seq_tile(two_q, seq, tiles, t, is_v);
+                if (!KV8 && is_v != values) continue;
                 if (!KV8 && is_v && t == tiles - 1) mbar_drain(&bar.last_v, 0);
-                else mbar_drain(KV8 ? &bar.raw_full[is_v][t & 3] : &bar.full[is_v][t & 3], (t >> 2) & 1);
+                else if (seq >= issued - NB) mbar_drain(KV8 ? &bar.raw_full[is_v][t & 3] : &bar.full[is_v][t & 3], (t >> 2) & 1);
             }
         }
     } else if (warp == W_MMA) {
-        if (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (S::SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::R_OTHER));
         // ---- products, all by one thread
         constexpr uint32_t type = MB ? (1u << 7) | (1u << 10) : 0u;
         constexpr uint32_t id_s = umma_idesc(128, BN, 0, 0) | type, id_o = umma_idesc(128, D, 0, 1) | type;
@@ -324,7 +336,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             const uint64_t q_desc = desc_kmajor(smem_addr(smem)), k_desc = desc_kmajor(smem_addr(ring)),
                            v_desc = desc_mnmajor(smem_addr(ring), BN * 128);
             auto scores = [&](int j) {
-                const int t = two_q ? j >> 1 : j, seq = seq_k(two_q, t), slot = seq % SLOTS;
+                const int t = two_q ? j >> 1 : j, slot = slot_of(seq_k(two_q, t));
                 if (!wait_one(&bar.full[0][t & 3], (t >> 2) & 1, abort)) return false;
                 tc_fence_after();
                 const uint64_t qd = q_desc + (two_q ? (j & 1) * (S::QTILE / 16) : 0), kd = k_desc + slot * (TILE / 16);
@@ -336,7 +348,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                 return true;
             };
             auto outputs = [&](int j) {
-                const int t = two_q ? j >> 1 : j, seq = seq_v(two_q, t, tiles), slot = seq % SLOTS;
+                const int t = two_q ? j >> 1 : j, slot = slot_of(seq_v(two_q, t, tiles));
                 if (!wait_one(&bar.full[1][t & 3], (t >> 2) & 1, abort)) return false;
                 if (!wait_one(&bar.p_full[j & 1], (j >> 1) & 1, abort)) return false;
                 tc_fence_after();
@@ -359,10 +371,10 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
         }
         __syncwarp();
     } else if (!KV8 && warp >= W_TMA) {
-        if (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (S::SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::R_OTHER));
         if (warp == W_TMA + 2 && tiles > 0) {
             // ---- the last tile's values past the range; its copy lands on a barrier of its own
-            const int slot = seq_v(two_q, tiles - 1, tiles) % SLOTS, live = u.hi - (u.lo + (tiles - 1) * BN);
+            const int slot = slot_of(seq_v(two_q, tiles - 1, tiles)), live = u.hi - (u.lo + (tiles - 1) * BN);
             if (wait_for(&bar.last_v, 0, abort)) {
                 for (int i = lane; i < (BN - live) * 8 * S::HALVES; i += 32) {
                     const int r = live + i / (8 * S::HALVES), c = i % (8 * S::HALVES);
@@ -373,56 +385,72 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                 if (lane == 0) mbar_arrive(&bar.full[1][(tiles - 1) & 3]);
             }
         }
-    } else if (KV8 && warp >= W_TMA) {
-        if (NS == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        // ---- 8-bit tiles to fp16
-        const int group = tid - (W_TMA + 2) * 32 >= S::CVT, c = tid - (W_TMA + 2) * 32 - (group ? S::CVT : 0);  // 0: keys, 1: values
-        const int sub_log2 = min(a.p.page_shift, BN == 128 ? 7 : 6), sub_rows = 1 << sub_log2;  // tokens of a box
-        int ref_most = 0;
+    } else if (KV8 && warp >= W_TMA && warp < W_TMA + 4) {
+        if (S::SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::R_OTHER));
+        // ---- the tokens' powers of two, up to four tiles ahead: a warp for the keys, one for the values
+        const bool is_v = warp == W_TMA + 3;
+        int most = 0;  // the values' largest exponent so far
         for (int t = 0; t < tiles; ++t) {
-            const bool is_v = group;
-            const int seq = is_v ? seq_v(two_q, t, tiles) : seq_k(two_q, t), live = min(BN, u.hi - (u.lo + t * BN));
-            const int slot = seq % SLOTS, rs = seq % (KV8 ? S::RAWS : 1);
-            if (!wait_for(&bar.raw_full[is_v][t & 3], (t >> 2) & 1, abort)) break;
-            // exponents of tokens 4 lane .. + 3, in every warp; bytes past the range are not the request's
-            const bool here = 4 * lane < live;
-            const unsigned mask = live - 4 * lane >= 4 ? 0xffffffffu : here ? (1u << (8 * (live - 4 * lane))) - 1u : 0u;
-            const unsigned char *at = exps + rs * 2048 + (4 * lane >> sub_log2) * 128 + (4 * lane & (sub_rows - 1));
-            const unsigned ev = here ? *reinterpret_cast<const unsigned *>(at + 1024) & mask : 0;
-            const unsigned ek = here && !is_v ? *reinterpret_cast<const unsigned *>(at) & mask : 0;
+            // exponents of tokens 4 lane .. + 3; bytes past the range are not the request's
+            const int j = u.lo + t * BN + 4 * lane, live = u.hi - j;
+            unsigned ek = 0, ev = 0;
+            if (4 * lane < BN && live > 0) {
+                const int pg = pool_page(a.p, u.b, j);
+                if (pg >= 0) {
+                    const long long at = ((((long long)pg * a.p.heads + u.h)) << a.p.page_shift) + (j & ((1 << a.p.page_shift) - 1));
+                    const unsigned mask = live >= 4 ? 0xffffffffu : (1u << (8 * live)) - 1u;
+                    ev = __ldg(reinterpret_cast<const unsigned *>(a.ve + at)) & mask;
+                    if (!is_v) ek = __ldg(reinterpret_cast<const unsigned *>(a.ke + at)) & mask;
+                }
+            }
             auto largest = [](unsigned e) {
                 const unsigned m = __vmaxu4(e, e >> 16);
                 return (int)__reduce_max_sync(0xffffffffu, max(m & 0xffu, (m >> 8) & 0xffu));
             };
-            ref_most = max(ref_most, largest(ev));
-            const int R = is_v ? ref_most : largest(ek);
-            const unsigned e4 = is_v ? ev : ek;
-            if (seq >= SLOTS) {
-                int t0;
-                bool v0;
-                seq_tile(two_q, seq - SLOTS, tiles, t0, v0);
-                if (!wait_for(&bar.empty[v0][t0 & 3], (t0 >> 2) & 1, abort)) break;
-            }
-            if (!is_v && c == 0) {  // the softmax learns both with the keys (t - 4 is past when a slot is free for t)
-                bar.k_ref[t & 3] = R;
-                bar.v_ref[t & 3] = ref_most;
-                mbar_arrive(&bar.ref_full[t & 3]);
-            }
-            // 2^(E - R) of each token in fp16, twice (subnormal below 2^-14, zero below 2^-24), a copy in every warp
-            unsigned *mine = reinterpret_cast<unsigned *>(smem + S::OFF_POW) + (warp - W_TMA - 2) * BN;
+            most = max(most, largest(ev));
+            const int R = is_v ? most : largest(ek);
+            // tile t - 4 is done with: its values multiplied (so its softmax is past), its keys or values turned
+            if (t >= 4 && (!wait_for(&bar.empty[1][t & 3], ((t - 4) >> 2) & 1, abort) ||
+                           !wait_for(&bar.raw_empty[is_v][t & 3], ((t - 4) >> 2) & 1, abort)))
+                break;
             if (4 * lane < BN) {
+                // 2^(E - R) in fp16, twice: subnormal below 2^-14, zero below 2^-24
                 unsigned f[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int E = (int)((e4 >> (8 * e)) & 0xffu) - R;
+                    const int E = (int)(((is_v ? ev : ek) >> (8 * e)) & 0xffu) - R;
                     f[e] = (E >= -14 ? (unsigned)(15 + E) << 10 : E >= -24 ? 1u << (24 + E) : 0u) * 0x10001u;
                 }
-                *reinterpret_cast<uint4 *>(mine + 4 * lane) = make_uint4(f[0], f[1], f[2], f[3]);
+                *reinterpret_cast<uint4 *>(smem + S::OFF_POW + ((is_v * 4 + (t & 3)) * BN + 4 * lane) * 4) = make_uint4(f[0], f[1], f[2], f[3]);
+            }
+            if (!is_v && lane == 0) {  // the softmax learns both
+                bar.k_ref[t & 3] = R;
+                bar.v_ref[t & 3] = most;
+                mbar_arrive(&bar.ref_full[t & 3]);
             }
             __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.pow_full[is_v][t & 3]);
+        }
+    } else if (KV8 && warp >= W_TMA + 4) {
+        if (S::SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::R_OTHER));
+        // ---- 8-bit tiles to fp16
+        const bool is_v = tid - (W_TMA + 4) * 32 >= S::CVT;
+        const int c = tid - (W_TMA + 4) * 32 - (is_v ? S::CVT : 0);
+        for (int t = 0; t < tiles; ++t) {
+            const int seq = is_v ? seq_v(two_q, t, tiles) : seq_k(two_q, t), live = min(BN, u.hi - (u.lo + t * BN));
+            const int slot = slot_of(seq), rs = seq % (KV8 ? S::RAWS : 1);
+            if (seq >= slots) {
+                int t0;
+                bool v0;
+                seq_tile(two_q, seq - slots, tiles, t0, v0);
+                if (!wait_for(&bar.empty[v0][t0 & 3], (t0 >> 2) & 1, abort)) break;
+            }
+            if (!wait_for(&bar.pow_full[is_v][t & 3], (t >> 2) & 1, abort)) break;
+            if (!wait_for(&bar.raw_full[is_v][t & 3], (t >> 2) & 1, abort)) break;
+            const unsigned *mine = reinterpret_cast<const unsigned *>(smem + S::OFF_POW) + (is_v * 4 + (t & 3)) * BN;
             const unsigned char *src = raw + rs * S::RAW;
             unsigned char *dst = ring + slot * TILE;
-            constexpr int CHUNKS = BN * D / 16, PER = KV8 ? (CHUNKS + S::CVT - 1) / (KV8 ? S::CVT : 1) : 1, BATCH = 4;
+            constexpr int CHUNKS = BN * D / 16, PER = KV8 ? (CHUNKS + S::CVT - 1) / (KV8 ? S::CVT : 1) : 1, BATCH = 2;
 #pragma unroll
             for (int i0 = 0; i0 < PER; i0 += BATCH) {
                 uint4 w[BATCH];
@@ -460,10 +488,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
         }
     } else {
         // ---- softmax: a thread per row
-        if (NS == 2) {
-            if (KV8) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-            else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-        }
+        if (S::SPLIT) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::R_SOFTMAX));
         const int s = warp / 4, row = tid % 128;
         const int r_unit = two_q ? s * mq_rows + row : row;  // this thread's row of the unit
         const int tok = (row0 + r_unit) / a.G, pos = u.first + tok;
@@ -476,7 +501,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             ok = wait_for(&bar.q_full, 0, abort);
             if (two_q || s == 0) {
                 unsigned char *mine = smem + (two_q ? s * S::QTILE : 0) + row * 128;
-                constexpr int N = 8 * S::HALVES < 16 ? 8 * S::HALVES : 16;  // chunks held at a time
+                constexpr int N = 8;  // chunks held at a time
                 float big = 0.f;
                 uint4 w[N];
 #pragma unroll 1
@@ -523,9 +548,10 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             const uint32_t s_addr = tm + lanes + (j & 1) * BN, p_addr = tm + lanes + S::COL_P + (j & 1) * S::P_STEP;
             if (!wait_for(&bar.s_full[j & 1], (j >> 1) & 1, abort)) { ok = false; break; }
             tc_fence_after();
-            uint32_t x[BN / 32][32];
+            constexpr int HELD = S::TWICE ? 2 : BN / 32;  // groups of 32 columns held in registers
+            uint32_t x[HELD][32];
 #pragma unroll
-            for (int i = 0; i < BN / 32; ++i) tmem_ld32_start(s_addr + 32 * i, x[i]);
+            for (int i = 0; i < HELD; ++i) tmem_ld32_start(s_addr + 32 * i, x[i]);
             float factor = q_factor;
             int ref_now = 0;
             if (KV8) {
@@ -535,24 +561,34 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             }
             tmem_wait_ld(x);
             if (!ok) break;
-            if (j0 + BN - 1 > pos_first || j0 + BN > u.hi || (a.window && j0 <= pos_last - a.window)) {
-                // columns least < i <= most are seen, as bits of each 32
-                const int most = min(pos, u.hi - 1) - j0, least = a.window ? pos - a.window - j0 : -1;
+            // columns least < i <= most are seen, as bits of each 32
+            const bool edge = j0 + BN - 1 > pos_first || j0 + BN > u.hi || (a.window && j0 <= pos_last - a.window);
+            const int most = min(pos, u.hi - 1) - j0, least = a.window ? pos - a.window - j0 : -1;
+            auto hide = [&](uint32_t(&y)[32], int i) {
+                const int up = most - 32 * i, down = least - 32 * i;
+                const unsigned keep = (up >= 31 ? 0xffffffffu : up < 0 ? 0u : (2u << up) - 1u) &
+                                      ~(down >= 31 ? 0xffffffffu : down < 0 ? 0u : (2u << down) - 1u);
 #pragma unroll
-                for (int i = 0; i < BN / 32; ++i) {
-                    const int up = most - 32 * i, down = least - 32 * i;
-                    const unsigned keep = (up >= 31 ? 0xffffffffu : up < 0 ? 0u : (2u << up) - 1u) &
-                                          ~(down >= 31 ? 0xffffffffu : down < 0 ? 0u : (2u << down) - 1u);
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) x[i][e] = keep & (1u << e) ? x[i][e] : 0xff800000u;  // -inf
-                }
-            }
+                for (int e = 0; e < 32; ++e) y[e] = keep & (1u << e) ? y[e] : 0xff800000u;  // -inf
+            };
             float b[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < BN; i += 8)
+            for (int i0 = 0; i0 < BN / 32; i0 += HELD) {
+                if (i0 > 0) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    b[e] = fmaxf(fmaxf(b[e], __uint_as_float(x[i / 32][i % 32 + 2 * e])), __uint_as_float(x[i / 32][i % 32 + 2 * e + 1]));
+                    for (int i = 0; i < HELD; ++i) tmem_ld32_start(s_addr + 32 * (i0 + i), x[i]);
+                    tmem_wait_ld(x);
+                }
+                if (edge) {
+#pragma unroll
+                    for (int i = 0; i < HELD; ++i) hide(x[i], i0 + i);
+                }
+#pragma unroll
+                for (int i = 0; i < HELD * 32; i += 8)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        b[e] = fmaxf(fmaxf(b[e], __uint_as_float(x[i / 32][i % 32 + 2 * e])), __uint_as_float(x[i / 32][i % 32 + 2 * e + 1]));
+            }
             const float big = fmaxf(fmaxf(b[0], b[1]), fmaxf(b[2], b[3])) * factor;
             if (!any) {
                 any = true;
@@ -586,15 +622,26 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             const float base = m == -INFINITY ? 0.f : m;
             const float2 f2 = make_float2(factor, factor), b2 = make_float2(-base, -base);
             float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            if (HELD < BN / 32) {
+                uint32_t(&y)[1][32] = reinterpret_cast<uint32_t(&)[1][32]>(x[0]);
+                tmem_ld32_start(s_addr, x[0]);
+                tmem_wait_ld(y);
+                if (edge) hide(x[0], 0);
+            }
 #pragma unroll
             for (int i = 0; i < BN / 32; ++i) {
-                uint32_t p[16];
+                uint32_t p[16], (&now)[32] = x[HELD < BN / 32 ? i & 1 : i], (&next)[32] = x[HELD < BN / 32 ? (i + 1) & 1 : 0];
+                if (HELD < BN / 32 && i + 1 < BN / 32) tmem_ld32_start(s_addr + 32 * (i + 1), next);
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
-                    float2 y = __ffma2_rn(make_float2(__uint_as_float(x[i][e]), __uint_as_float(x[i][e + 1])), f2, b2);
+                    float2 y = __ffma2_rn(make_float2(__uint_as_float(now[e]), __uint_as_float(now[e + 1])), f2, b2);
                     y = make_float2(ex2(y.x), ex2(y.y));
                     l2[(e >> 1) & 1] = __fadd2_rn(l2[(e >> 1) & 1], y);
                     p[e / 2] = pack2<MB>(y.x, y.y);
+                }
+                if (HELD < BN / 32 && i + 1 < BN / 32) {
+                    tmem_wait_ld(reinterpret_cast<uint32_t(&)[1][32]>(next));
+                    if (edge) hide(next, i + 1);
                 }
                 tmem_st16(p_addr + 16 * i, p);
             }
@@ -608,7 +655,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
         tc_fence_after();
         const float unit = KV8 ? ex2((float)(ref - 127)) : 1.f;
         constexpr int PITCH = D + 4;
-        unsigned char *mine = ring + 8192;  // (the first bytes may hold rows on their way out)
+        unsigned char *mine = smem + S::OFF_RING + 8192;  // (rows on their way out may take the bytes before)
         float *mo = reinterpret_cast<float *>(mine);
         float2 *ml = reinterpret_cast<float2 *>(mine + 128 * PITCH * 4);
         const bool merge = NS == 2 && !two_q;
@@ -651,38 +698,36 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             const int at = (u.s + tok) * (a.p.heads * a.G) + u.h * a.G + (row0 + r_unit - tok * a.G);
             float *part = a.part + (size_t)(u.slot + u.c) * a.M * (D + 2);
             const bool bf = KV8 ? io_bf : BF;
-            // A warp's 32 rows x 64 columns pass through shared memory (the q tiles' place), so that 16 lanes
+            // A warp's 32 rows x EC columns pass through shared memory (the q tiles' place), so that EC / 4 lanes
             // write a row's neighbouring columns; a lane writing its own row would touch 32 lines a store.
-            float *stage = reinterpret_cast<float *>(smem) + warp * (32 * 68);
+            constexpr int EC = KV8 ? 32 : 64, ER = 128 / EC;  // columns at a time, rows a store
+            float *stage = reinterpret_cast<float *>(smem) + warp * (32 * (EC + 4));
 #pragma unroll 1
-            for (int d = 0; d < D; d += 64) {
-                uint32_t y[2][32];
-                float z[64];
+            for (int d = 0; d < D; d += EC) {
+                uint32_t y[EC / 32][32];
                 if (any) {
-                    tmem_ld32_start(o_addr + d, y[0]);
-                    tmem_ld32_start(o_addr + d + 32, y[1]);
+#pragma unroll
+                    for (int i = 0; i < EC / 32; ++i) tmem_ld32_start(o_addr + d + 32 * i, y[i]);
                     tmem_wait_ld(y);
                 }
 #pragma unroll
-                for (int e = 0; e < 64; ++e) z[e] = any ? f0 * __uint_as_float(y[e / 32][e % 32]) : 0.f;
-                if (other) {
-#pragma unroll
-                    for (int e = 0; e < 64; e += 4) {
+                for (int e = 0; e < EC; e += 4) {
+                    float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (any)
+                        z = make_float4(f0 * __uint_as_float(y[e / 32][e % 32]), f0 * __uint_as_float(y[e / 32][e % 32 + 1]),
+                                        f0 * __uint_as_float(y[e / 32][e % 32 + 2]), f0 * __uint_as_float(y[e / 32][e % 32 + 3]));
+                    if (other) {
                         const float4 w = *reinterpret_cast<const float4 *>(mo + row * PITCH + d + e);
-                        z[e] = fmaf(f1, w.x, z[e]);
-                        z[e + 1] = fmaf(f1, w.y, z[e + 1]);
-                        z[e + 2] = fmaf(f1, w.z, z[e + 2]);
-                        z[e + 3] = fmaf(f1, w.w, z[e + 3]);
+                        z = make_float4(fmaf(f1, w.x, z.x), fmaf(f1, w.y, z.y), fmaf(f1, w.z, z.z), fmaf(f1, w.w, z.w));
                     }
+                    *reinterpret_cast<float4 *>(stage + lane * (EC + 4) + e) = z;
                 }
-#pragma unroll
-                for (int e = 0; e < 64; e += 4) *reinterpret_cast<float4 *>(stage + lane * 68 + e) = make_float4(z[e], z[e + 1], z[e + 2], z[e + 3]);
                 __syncwarp();
 #pragma unroll 8
-                for (int i = 0; i < 16; ++i) {
-                    const int r = 2 * i + lane / 16, e = 4 * (lane % 16), ru = r_unit - lane + r;
+                for (int i = 0; i < 32 / ER; ++i) {
+                    const int r = ER * i + lane / (EC / 4), e = 4 * (lane % (EC / 4)), ru = r_unit - lane + r;
                     const int row_at = __shfl_sync(0xffffffffu, at, r), r_tile = row - lane + r;
-                    const float4 w = *reinterpret_cast<const float4 *>(stage + r * 68 + e);
+                    const float4 w = *reinterpret_cast<const float4 *>(stage + r * (EC + 4) + e);
                     if (r_tile >= mq_rows || ru >= rows) continue;
                     if (final) {
                         uint2 h;
@@ -734,26 +779,14 @@ bool q_map(CUtensorMap *m, const AttnArgs &a, int D) {
                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// [pages][heads * page] exponent bytes: boxes of `rows` bytes, zeros past the last page.
-bool exp_map(CUtensorMap *m, const void *base, const AttnArgs &a, int rows) {
-    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-    if (!enc) return false;
-    const cuuint64_t row = (cuuint64_t)a.p.heads << a.p.page_shift;
-    const cuuint64_t dims[2] = {row, (cuuint64_t)a.p.pages}, strides[1] = {row};
-    const cuuint32_t box[2] = {(cuuint32_t)rows, 1}, es[2] = {1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int D, bool BF, bool KV8>
 dn_status launch_tile(const AttnArgs &a, bool io_bf, unsigned grid, cudaStream_t st) {
     using S = TileShape<D, KV8>;
     const int rows = 1 << a.p.page_shift < S::BN ? 1 << a.p.page_shift : S::BN;
-    CUtensorMap mq, mk, mv, mke = {}, mve = {};
+    CUtensorMap mq, mk, mv;
     if (!q_map(&mq, a, D) || !pool_map(&mk, a.kc, a, D, KV8 ? 1 : 2, rows) || !pool_map(&mv, a.vc, a, D, KV8 ? 1 : 2, rows)) return DN_ERR_CUDA;
-    if (KV8 && (!exp_map(&mke, a.ke, a, rows) || !exp_map(&mve, a.ve, a, rows))) return DN_ERR_CUDA;
     cudaFuncSetAttribute(attn_tile_kernel<D, BF, KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
-    launch_pdl(attn_tile_kernel<D, BF, KV8>, dim3(grid), dim3(S::THREADS), S::BYTES, st, a, mq, mk, mv, mke, mve, io_bf);
+    launch_pdl(attn_tile_kernel<D, BF, KV8>, dim3(grid), dim3(S::THREADS), S::BYTES, st, a, mq, mk, mv, io_bf);
     return DN_OK;
 }
 
