@@ -87,7 +87,8 @@ def load_library(path=None):
 
 def _stream(stream):
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the handle that torch.cuda.current_stream().cuda_stream gives, without the Stream object (3 us)
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -313,31 +314,52 @@ def dn_context_drafts(context, lengths, n_max=4, n_min=1, K=8, drafts=None, coun
     return drafts, count, match_len
 
 
+_I32, _U8, _E4M3 = torch.int32, torch.uint8, torch.float8_e4m3fn
+
+
 def _kv_pool(start, kv_len, page_table, k_cache, v_cache, k_exp, v_exp):
-    """Checks the paged cache's tensors; returns (B, heads, D, page, max_pages, pages)."""
-    _require(k_cache.dim() == 4 and v_cache.shape == k_cache.shape and v_cache.dtype == k_cache.dtype,
+    """Checks the paged cache's tensors; returns (B, heads, D, page, max_pages, pages, cache dtype).
+
+    One expression for the good case (these checks are a good part of a small call's time); what is
+    wrong is looked for only if something is.
+    """
+    shape, dt = k_cache.shape, k_cache.dtype
+    table = page_table.shape
+    if (len(shape) == 4 and len(table) == 2 and v_cache.shape == shape and v_cache.dtype is dt
+            and start.shape == (table[0] + 1,) and kv_len.shape == (table[0],)
+            and start.dtype is _I32 and kv_len.dtype is _I32 and page_table.dtype is _I32
+            and start.is_cuda and kv_len.is_cuda and page_table.is_cuda and k_cache.is_cuda and v_cache.is_cuda
+            and start.is_contiguous() and kv_len.is_contiguous() and page_table.is_contiguous()
+            and k_cache.is_contiguous() and v_cache.is_contiguous()
+            and (k_exp is None and v_exp is None and dt in _KV_DT if dt is not _E4M3 else
+                 k_exp is not None and v_exp is not None and k_exp.dtype is _U8 and v_exp.dtype is _U8
+                 and k_exp.shape == shape[:3] and v_exp.shape == shape[:3] and k_exp.is_cuda and v_exp.is_cuda
+                 and k_exp.is_contiguous() and v_exp.is_contiguous())):
+        return table[0], shape[1], shape[3], shape[2], table[1], shape[0], _KV_DT[dt]
+    _require(len(shape) == 4 and v_cache.shape == shape and v_cache.dtype == dt,
              "k_cache, v_cache [pages,heads,page,D] of one dtype")
-    pages, heads, page, D = k_cache.shape
-    B, max_pages = page_table.shape
     _dev(start, kv_len, page_table, k_cache, v_cache, k_exp, v_exp)
     _require(start.dtype == kv_len.dtype == page_table.dtype == torch.int32, "start, kv_len, page_table int32")
-    _require(start.shape == (B + 1,) and kv_len.shape == (B,), "start [B+1], kv_len [B], page_table [B,max_pages]")
-    _require(k_cache.dtype in _KV_DT, "k_cache, v_cache fp16, bf16 or float8_e4m3fn")
-    if k_cache.dtype == torch.float8_e4m3fn:
-        _require(k_exp is not None and v_exp is not None and k_exp.dtype == v_exp.dtype == torch.uint8
-                 and k_exp.shape == v_exp.shape == (pages, heads, page), "an e4m3 cache has k_exp, v_exp [pages,heads,page] uint8")
-    else:
-        _require(k_exp is None and v_exp is None, "k_exp, v_exp go with an e4m3 cache")
-    return B, heads, D, page, max_pages, pages
+    _require(dt in _KV_DT, "k_cache, v_cache fp16, bf16 or float8_e4m3fn")
+    _require(dt == _E4M3 or (k_exp is None and v_exp is None), "k_exp, v_exp go with an e4m3 cache")
+    _require(dt != _E4M3 or (k_exp is not None and v_exp is not None and k_exp.dtype == v_exp.dtype == torch.uint8
+                             and k_exp.shape == v_exp.shape == shape[:3]),
+             "an e4m3 cache has k_exp, v_exp [pages,heads,page] uint8")
+    raise ValueError("start [B+1], kv_len [B], page_table [B,max_pages]")
 
 
 def _rows(t, heads, D, name):
-    """Checks packed rows [total, heads, D], dense inside a row; returns (total, row stride in elements)."""
+    """Checks packed rows [total, heads, D], dense inside a row; returns (total, row stride in elements, dtype)."""
+    shape, dt = t.shape, t.dtype
+    if len(shape) == 3 and shape[1] == heads and shape[2] == D and t.is_cuda and dt in _KV_DT:
+        if t.is_contiguous():
+            return shape[0], heads * D, _KV_DT[dt]
+        if t.stride(2) == 1 and (heads == 1 or t.stride(1) == D):
+            return shape[0], t.stride(0) if shape[0] > 1 else heads * D, _KV_DT[dt]
     _require(t.is_cuda, "all tensors must be CUDA tensors")
-    _require(t.dim() == 3 and t.shape[1] == heads and t.shape[2] == D, "%s [total,heads,D]" % name)
-    _require(t.stride(2) == 1 and (heads == 1 or t.stride(1) == D), "%s dense inside a row" % name)
-    _require(t.dtype in _KV_DT, "%s fp16 or bf16" % name)
-    return t.shape[0], t.stride(0) if t.shape[0] > 1 else heads * D
+    _require(len(shape) == 3 and shape[1] == heads and shape[2] == D, "%s [total,heads,D]" % name)
+    _require(dt in _KV_DT, "%s fp16 or bf16" % name)
+    raise ValueError("%s dense inside a row" % name)
 
 
 def dn_kv_append(k, v, start, kv_len, page_table, k_cache, v_cache, k_exp=None, v_exp=None, stream=None):
@@ -347,15 +369,17 @@ def dn_kv_append(k, v, start, kv_len, page_table, k_cache, v_cache, k_exp=None, 
     [pages,heads,page,D] in k's dtype, or float8_e4m3fn with k_exp, v_exp [pages,heads,page] uint8.
     k and v may be slices of a wider projection (rows dense inside). Returns (k_cache, v_cache).
     """
-    B, heads, D, page, max_pages, pages = _kv_pool(start, kv_len, page_table, k_cache, v_cache, k_exp, v_exp)
-    total, ks = _rows(k, heads, D, "k")
-    total_v, vs = _rows(v, heads, D, "v")
-    _require(total_v == total and v.dtype == k.dtype, "v like k")
-    st = load_library().dn_kv_append(
-        B, total, heads, D, page, max_pages, pages, _KV_DT[k.dtype], _KV_DT[k_cache.dtype], _ptr(k), _ptr(v), ks, vs,
-        _ptr(start), _ptr(kv_len), _ptr(page_table), _ptr(k_cache), _ptr(v_cache), _ptr(k_exp), _ptr(v_exp),
-        _stream(stream))
-    _check("dn_kv_append", st)
+    B, heads, D, page, max_pages, pages, cdt = _kv_pool(start, kv_len, page_table, k_cache, v_cache, k_exp, v_exp)
+    total, ks, dt = _rows(k, heads, D, "k")
+    total_v, vs, dt_v = _rows(v, heads, D, "v")
+    if total_v != total or dt_v != dt:
+        raise ValueError("v like k")
+    st = (_lib or load_library()).dn_kv_append(
+        B, total, heads, D, page, max_pages, pages, dt, cdt, k.data_ptr(), v.data_ptr(), ks, vs,
+        start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_exp),
+        _ptr(v_exp), _stream(stream))
+    if st:
+        _check("dn_kv_append", st)
     return k_cache, v_cache
 
 
@@ -364,14 +388,16 @@ def dn_kv_gather(start, kv_len, page_table, k_cache, v_cache, k_exp, v_exp, k, v
 
     The cache's tensors as for dn_kv_append (k_exp, v_exp None unless it is e4m3). Returns (k, v).
     """
-    B, heads, D, page, max_pages, pages = _kv_pool(start, kv_len, page_table, k_cache, v_cache, k_exp, v_exp)
+    B, heads, D, page, max_pages, pages, cdt = _kv_pool(start, kv_len, page_table, k_cache, v_cache, k_exp, v_exp)
+    total, _, dt = _rows(k, heads, D, "k")
+    if v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("v like k")
     _dev(k, v)
-    total, _ = _rows(k, heads, D, "k")
-    _require(v.shape == k.shape and v.dtype == k.dtype, "v like k")
-    st = load_library().dn_kv_gather(
-        B, total, heads, D, page, max_pages, pages, _KV_DT[k.dtype], _KV_DT[k_cache.dtype], _ptr(start), _ptr(kv_len),
-        _ptr(page_table), _ptr(k_cache), _ptr(v_cache), _ptr(k_exp), _ptr(v_exp), _ptr(k), _ptr(v), _stream(stream))
-    _check("dn_kv_gather", st)
+    st = (_lib or load_library()).dn_kv_gather(
+        B, total, heads, D, page, max_pages, pages, dt, cdt, start.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_exp), _ptr(v_exp), k.data_ptr(), v.data_ptr(), _stream(stream))
+    if st:
+        _check("dn_kv_gather", st)
     return k, v
 
 
@@ -394,10 +420,11 @@ def dn_attn_paged(q, start, kv_len, page_table, k_cache, v_cache, k_exp=None, v_
     D ** -0.5; window is how many tokens a row looks back, itself included (0: all). q may be a slice of
     a wider projection. Returns (out [total,heads,D] in q's dtype, lse [total,heads] fp32).
     """
-    B, heads_kv, D, page, max_pages, pages = _kv_pool(start, kv_len, page_table, k_cache, v_cache, k_exp, v_exp)
-    _require(q.dim() == 3 and q.shape[1] % heads_kv == 0 and q.shape[1] > 0, "q's heads a multiple of the cache's")
+    B, heads_kv, D, page, max_pages, pages, cdt = _kv_pool(start, kv_len, page_table, k_cache, v_cache, k_exp, v_exp)
+    if q.dim() != 3 or q.shape[1] % heads_kv or q.shape[1] < 1:
+        raise ValueError("q's heads a multiple of the cache's")
     heads = q.shape[1]
-    total, qs = _rows(q, heads, D, "q")
+    total, qs, dt = _rows(q, heads, D, "q")
     if out is None:
         out = torch.empty((total, heads, D), dtype=q.dtype, device=q.device)
     if lse is None:
@@ -405,14 +432,17 @@ def dn_attn_paged(q, start, kv_len, page_table, k_cache, v_cache, k_exp=None, v_
     if workspace is None:
         workspace = attn_workspace(q, k_cache, page_table)
     _dev(out, lse, workspace)
-    _require(out.shape == q.shape and out.dtype == q.dtype, "out [total,heads,D] in q's dtype")
-    _require(lse.shape == (total, heads) and lse.dtype == torch.float32, "lse [total,heads] fp32")
-    st = load_library().dn_attn_paged(
-        B, total, heads_kv, heads // heads_kv, D, page, max_pages, pages, _KV_DT[q.dtype], _KV_DT[k_cache.dtype],
-        _ptr(q), qs, _ptr(start), _ptr(kv_len), _ptr(page_table), _ptr(k_cache), _ptr(v_cache), _ptr(k_exp),
-        _ptr(v_exp), float(D ** -0.5 if scale is None else scale), int(window), _ptr(out), _ptr(lse), _ptr(workspace),
+    if out.shape != q.shape or out.dtype is not q.dtype:
+        raise ValueError("out [total,heads,D] in q's dtype")
+    if lse.shape != (total, heads) or lse.dtype is not torch.float32:
+        raise ValueError("lse [total,heads] fp32")
+    st = (_lib or load_library()).dn_attn_paged(
+        B, total, heads_kv, heads // heads_kv, D, page, max_pages, pages, dt, cdt, q.data_ptr(), qs, start.data_ptr(),
+        kv_len.data_ptr(), page_table.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_exp), _ptr(v_exp),
+        D ** -0.5 if scale is None else scale, window, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _stream(stream))
-    _check("dn_attn_paged", st)
+    if st:
+        _check("dn_attn_paged", st)
     return out, lse
 
 
