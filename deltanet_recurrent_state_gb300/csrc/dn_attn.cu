@@ -611,7 +611,7 @@ extern "C" size_t dn_attn_workspace_bytes(int B, int total, int heads_kv, int gr
     size_t most = 0;
     for (int kv8 = 0; kv8 < 2; ++kv8) {
         const AttnPlan p = attn_plan(B, total, group, D, kv8);
-        most = std::max(most, (size_t)2 * std::max(p.target, p.wave) * p.M * (D + 2) * sizeof(float));
+        most = std::max(most, (size_t)(2 * std::max(p.target, p.wave) + 64) * p.M * (D + 2) * sizeof(float));
     }
     return most;
 }

@@ -16,8 +16,8 @@
 // Partials. A tile seen in one range is finished by its unit. Otherwise every range leaves the running
 // maximum, the sum and the unnormalised output of its rows (32 bits) in a slot of the workspace,
 // and attn_join_kernel adds them in the order of the ranges, so results repeat bit for bit. Only
-// requests with at least two ranges own slots, and those have fewer than 2 * max(target, wave) of them
-// (a request of span > C has fewer than 2 span / C ranges), whatever B and the lengths are.
+// requests with at least two ranges own slots, and those have about 2 * max(target, wave) of them at
+// most (a request of span > C has fewer than 2 span / C ranges), whatever B and the lengths are.
 #pragma once
 
 #include "dn.h"
@@ -58,82 +58,116 @@ __host__ __device__ inline long long attn_tiles_bound(int B, int total, int G, i
     const long long rows = (long long)total * G;
     return rows / M + (B < total ? B : total);
 }
+// a / b for a >= 0, b > 0. Most of a unit's search is divisions, and an integer one takes about 100 cycles:
+// below 2^21 the quotient of 32-bit floats (2 units in the last place) is off by less than one before it is
+// cut, so by one at most before the correction.
+__device__ __forceinline__ int attn_div(int a, int b) {
+    if (a >= 1 << 21 || b >= 1 << 24) return a / b;
+    int q = (int)__fdividef((float)a, (float)b);
+    const int r = a - q * b;
+    q += r >= b ? 1 : r < 0 ? -1 : 0;
+    return q;
+}
+__device__ __forceinline__ int attn_ceil_div(int a, int b) { return attn_div(a + b - 1, b); }
+
 // A request's packed rows, cached tokens, tiles and the most tokens that one of its tiles sees.
-__device__ __forceinline__ void attn_request(const AttnArgs &a, int b, int &s, int &n, int &first, int &len, int &tiles,
-                                             int &span) {
-    packed_rows(a.p, b, s, n);
+struct AttnRequest {
+    int s, n, first, len, tiles, span;
+};
+__device__ __forceinline__ AttnRequest attn_request(const AttnArgs &a, int b) {
+    AttnRequest r;
+    packed_rows(a.p, b, r.s, r.n);
     const int held = min(max(__ldg(&a.p.kv_len[b]), 0), 1 << 30);
-    first = held - n;
-    len = min(held, a.p.max_pages << a.p.page_shift);
-    tiles = (n * a.G + a.M - 1) / a.M;  // (the host bounds total * heads by 2^31 - 1 - M)
-    span = a.window ? min(len, a.window + (a.M - 1) / a.G + 1 + a.align) : len;  // (window <= 2^30)
+    r.first = held - r.n;
+    r.len = min(held, a.p.max_pages << a.p.page_shift);
+    r.tiles = attn_ceil_div(r.n * a.G, a.M);  // (the host bounds total * heads by 2^31 - 1 - 1024)
+    r.span = a.window ? min(r.len, a.window + attn_div(a.M - 1, a.G) + 1 + a.align) : r.len;  // (window <= 2^30)
+    return r;
 }
 
 // The unit with this number (JOIN: the tile and head with this number among those of requests with
 // several ranges), found by one warp; false if there is none.
 template <bool JOIN>
 __device__ __forceinline__ bool attn_unit(const AttnArgs &a, int idx, AttnUnit &u) {
-    const int lane = threadIdx.x % 32, B = a.p.B;
+    const int lane = threadIdx.x % 32, B = a.p.B, unit_log2 = 31 - __clz(a.align);
+    AttnRequest r = {};
     long long work = 0;
     int whole = 0;  // tiles
-    int s = 0, n = 0, first = 0, len = 0, tiles = 0, span = 0;
-    for (int i = 0; i < B; i += 32) {
-        tiles = span = 0;
-        if (i + lane < B) attn_request(a, i + lane, s, n, first, len, tiles, span);
-        work += (long long)tiles * span;
-        whole += tiles;
-    }
+    if (B == 1) {   // (every lane has the one request: nothing to add up or to hand round)
+        r = attn_request(a, 0);
+        work = (long long)r.tiles * r.span;
+        whole = r.tiles;
+    } else {
+        for (int i = 0; i < B; i += 32) {
+            r = AttnRequest{};
+            if (i + lane < B) r = attn_request(a, i + lane);
+            work += (long long)r.tiles * r.span;
+            whole += r.tiles;
+        }
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) work += __shfl_xor_sync(0xffffffffu, work, off);
-    whole = __reduce_add_sync(0xffffffffu, whole);
+        for (int off = 16; off > 0; off >>= 1) work += __shfl_xor_sync(0xffffffffu, work, off);
+        whole = __reduce_add_sync(0xffffffffu, whole);
+    }
     const int target = 2 * (long long)whole * a.p.heads < a.wave ? a.wave : a.target;
-    // C = work * heads / target, rounded up to a multiple of align: in 32 bits unless the work is huge
-    work = work * a.p.heads + target - 1;
-    const long long C = work < 0x7fffffff ? (int)work / target : work / target;
-    const int most = max((int)min((C + a.align - 1) & ~(long long)(a.align - 1), 1ll << 30), a.min_range);
+    // C = work * heads / target in units of align tokens (2^24 at most); 2^-20 less, so that what fits is not
+    // rounded up, which the slots' margin covers
+    const int C = (int)fminf(ceilf(__fdividef((float)work * (float)a.p.heads, (float)target * (float)a.align) * (1.f - 0x1p-20f)), 16777215.f);
+    const int least = a.min_range >> unit_log2, most = max(C, least);
+    // equal ranges of at most `most`
+    auto cut = [&](int span, int &step) {
+        const int units = (span + a.align - 1) >> unit_log2;
+        step = units;
+        if (units > most) step = attn_ceil_div(units, attn_ceil_div(units, most));
+        step = max(step, least);
+        return units > step ? attn_ceil_div(units, step) : 1;
+    };
     int before = 0, slots_before = 0;
     for (int i = 0; i < B; i += 32) {
         if (B > 32) {  // (else the values of the loop above)
-            tiles = span = 0;
-            if (i + lane < B) attn_request(a, i + lane, s, n, first, len, tiles, span);
+            r = AttnRequest{};
+            if (i + lane < B) r = attn_request(a, i + lane);
         }
-        // equal ranges of at most `most` tokens (all at most 2^30)
-        const int cut = max(1, (span + most - 1) / most), range = max(a.min_range, ((span + cut - 1) / cut + a.align - 1) & ~(a.align - 1));
-        const int ranges = max(1, (span + range - 1) / range);
-        const int slots = ranges > 1 ? tiles * ranges * a.p.heads : 0;
-        const int units = JOIN ? (ranges > 1 ? tiles * a.p.heads : 0) : tiles * ranges * a.p.heads;
+        int step;
+        const int ranges = cut(r.span, step);
+        const int slots = ranges > 1 ? r.tiles * ranges * a.p.heads : 0;
+        const int units = JOIN ? (ranges > 1 ? r.tiles * a.p.heads : 0) : r.tiles * ranges * a.p.heads;
         int upto = units, slots_upto = slots;
+        if (B > 1) {
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, upto, off), y = __shfl_up_sync(0xffffffffu, slots_upto, off);
-            if (lane >= off) {
-                upto += x;
-                slots_upto += y;
+            for (int off = 1; off < 32; off <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, upto, off), y = __shfl_up_sync(0xffffffffu, slots_upto, off);
+                if (lane >= off) {
+                    upto += x;
+                    slots_upto += y;
+                }
             }
         }
         const unsigned past = __ballot_sync(0xffffffffu, idx < before + upto);
         if (past) {
             const int at = __ffs(past) - 1;
-            auto from = [&](int x) { return __shfl_sync(0xffffffffu, x, at); };
+            auto from = [&](int x) { return B == 1 ? x : __shfl_sync(0xffffffffu, x, at); };
             u.b = i + at;
-            u.s = from(s);
-            u.n = from(n);
-            u.first = from(first);
-            u.len = from(len);
-            const int T = from(tiles), R = from(ranges), step = from(range);
+            u.s = from(r.s);
+            u.n = from(r.n);
+            u.first = from(r.first);
+            u.len = from(r.len);
+            const int T = from(r.tiles), R = from(ranges);
+            step = from(step) << unit_log2;  // (2^30 + align at most)
             int local = idx - before - from(upto - units);
             // neighbours in the grid are tiles of one range, so they share its pages in L2; the
             // last tile of a prompt, which sees most, comes first
-            u.t = T - 1 - local % T;
-            local /= T;
-            u.c = JOIN ? 0 : local % R;
-            u.h = JOIN ? local : local / R;
+            int q = T > 1 ? attn_div(local, T) : local;
+            u.t = T - 1 - (local - q * T);
+            local = q;
+            q = JOIN || R == 1 ? local : attn_div(local, R);
+            u.c = JOIN ? 0 : local - q * R;
+            u.h = q;
             u.slot = slots_before + from(slots_upto - slots) + (u.h * T + u.t) * R;
             const int r0 = u.t * a.M, r1 = min(a.M, u.n * a.G - r0) - 1 + r0;
-            const int hi = min(max(u.first + r1 / a.G + 1, 0), u.len);
-            int lo = a.window ? max(u.first + r0 / a.G - a.window + 1, 0) : 0;
-            lo = min(lo & ~(a.align - 1), hi);  // (align is a power of two)
-            u.ranges = max(1, (hi - lo + step - 1) / step);
+            const int hi = min(max(u.first + attn_div(r1, a.G) + 1, 0), u.len);
+            int lo = a.window ? max(u.first + attn_div(r0, a.G) - a.window + 1, 0) : 0;
+            lo = min(lo & ~(a.align - 1), hi);
+            u.ranges = hi - lo > step ? attn_ceil_div(hi - lo, step) : 1;
             u.lo = u.c < u.ranges ? lo + u.c * step : hi;
             u.hi = hi - u.lo > step ? u.lo + step : hi;
             return true;
