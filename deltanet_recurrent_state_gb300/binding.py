@@ -421,9 +421,10 @@ def dn_attn_paged(q, start, kv_len, page_table, k_cache, v_cache, k_exp=None, v_
     a wider projection. Returns (out [total,heads,D] in q's dtype, lse [total,heads] fp32).
     """
     B, heads_kv, D, page, max_pages, pages, cdt = _kv_pool(start, kv_len, page_table, k_cache, v_cache, k_exp, v_exp)
-    if q.dim() != 3 or q.shape[1] % heads_kv or q.shape[1] < 1:
+    shape = q.shape
+    if len(shape) != 3 or shape[1] % heads_kv or shape[1] < 1:
         raise ValueError("q's heads a multiple of the cache's")
-    heads = q.shape[1]
+    heads = shape[1]
     total, qs, dt = _rows(q, heads, D, "q")
     if out is None:
         out = torch.empty((total, heads, D), dtype=q.dtype, device=q.device)
@@ -431,16 +432,18 @@ def dn_attn_paged(q, start, kv_len, page_table, k_cache, v_cache, k_exp=None, v_
         lse = torch.empty((total, heads), dtype=torch.float32, device=q.device)
     if workspace is None:
         workspace = attn_workspace(q, k_cache, page_table)
-    _dev(out, lse, workspace)
-    if out.shape != q.shape or out.dtype is not q.dtype:
+    if not (out.is_cuda and out.is_contiguous() and lse.is_cuda and lse.is_contiguous() and workspace.is_cuda
+            and workspace.is_contiguous()):
+        raise ValueError("out, lse and workspace are contiguous CUDA tensors")
+    if out.shape != shape or out.dtype is not q.dtype:
         raise ValueError("out [total,heads,D] in q's dtype")
-    if lse.shape != (total, heads) or lse.dtype is not torch.float32:
+    if lse.shape != shape[:2] or lse.dtype is not torch.float32:
         raise ValueError("lse [total,heads] fp32")
     st = (_lib or load_library()).dn_attn_paged(
         B, total, heads_kv, heads // heads_kv, D, page, max_pages, pages, dt, cdt, q.data_ptr(), qs, start.data_ptr(),
         kv_len.data_ptr(), page_table.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_exp), _ptr(v_exp),
         D ** -0.5 if scale is None else scale, window, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _stream(stream))
+        workspace.nbytes, _stream(stream))
     if st:
         _check("dn_attn_paged", st)
     return out, lse
