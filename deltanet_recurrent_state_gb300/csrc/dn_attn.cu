@@ -553,7 +553,7 @@ attn_join_kernel(const __grid_constant__ AttnArgs a, bool bf) {
 
 struct AttnPlan {
     bool tc;
-    int M, wave, target, align, min_range;
+    int M, wave, target, align, min_range, unit_cost, join_cost;
 };
 
 AttnPlan attn_plan(int B, int total, int G, int D, bool kv8) {
@@ -563,9 +563,9 @@ AttnPlan attn_plan(int B, int total, int G, int D, bool kv8) {
     // each of 4 key heads: D = 128 in 16 bits 218 us on warps and 201 in tiles, in 8 bits 198 and 349, D = 64 128 and 163.
     // D = 256 holds 16 rows a warp.
     if (rows > (D == 256 || (D == 128 && !kv8) ? 16 : 32) && G <= 128)
-        return {true, 128 / G * G * (D == 256 ? 1 : 2), kAttnSms, kAttnSms, D == 256 ? 64 : 128, 512};
+        return {true, 128 / G * G * (D == 256 ? 1 : 2), kAttnSms, kAttnSms, D == 256 ? 64 : 128, 512, 600, 200};
     const int resident = D == 256 ? (kv8 ? 2 : 1) : 3;  // CTAs an SM
-    return {false, rows <= 16 ? 16 : 32, resident * kAttnSms, 8 * kAttnSms, 64, 64};
+    return {false, rows <= 16 ? 16 : 32, resident * kAttnSms, 8 * kAttnSms, 64, 64, 400, 100};
 }
 
 template <int D, int MT, bool BF, bool KV8>
@@ -636,7 +636,7 @@ extern "C" dn_status dn_attn_paged(int B, int total, int heads_kv, int group, in
         workspace_bytes < dn_attn_workspace_bytes(B, total, heads_kv, group, D))
         return DN_ERR_INVALID_ARG;
     AttnPlan p = attn_plan(B, total, group, D, cache_dt == DN_E4M3);
-    if (pages == 0 || max_pages == 0) p = {false, 16, kAttnSms, kAttnSms, 64, 64};  // nothing is cached: no pool to copy from
+    if (pages == 0 || max_pages == 0) p = {false, 16, kAttnSms, kAttnSms, 64, 64, 400, 100};  // nothing is cached: no pool to copy from
     // At most this many units: few tiles are cut for one wave (CTAs without a unit cost their launch, 5 us for
     // 1,000 of the largest), and a table of few pages bounds the ranges of a tile.
     const long long whole = attn_tiles_bound(B, total, group, p.M) * heads_kv;
@@ -663,6 +663,9 @@ extern "C" dn_status dn_attn_paged(int B, int total, int heads_kv, int group, in
     a.wave = p.wave;
     a.target = p.target;
     a.min_range = p.min_range;
+    a.unit_cost = p.unit_cost;
+    a.join_cost = p.join_cost;
+    a.soft = !p.tc;
     const bool bf = io_dt == DN_BF16, kv8 = cache_dt == DN_E4M3;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
     if (p.tc && pages > 0 && max_pages > 0) {

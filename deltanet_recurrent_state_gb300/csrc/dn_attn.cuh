@@ -6,12 +6,12 @@
 //
 // Units. A unit is a tile, a key head and a range of cached tokens, the work of one CTA. Lengths are
 // known on the device only, so every CTA finds its own unit: its warps read the B requests' lengths,
-// sum the work (tiles x tokens x heads), take the range length C that makes so many units of it, and look
-// their unit up in the running count. If there are fewer tiles than half the CTAs that run at once, that
-// is one wave of equal ranges (a single request's long cache: D = 256, one token over 25,000, took 27.7 us so
-// and 39.5 in four waves); else it is a few waves, whose ends even out requests of all lengths (64
-// requests: 173 us against 191 in one wave). A request's ranges are of one length. The host sizes the grid
-// by a bound; CTAs past the last unit leave.
+// sum the work (tiles x tokens x heads), choose a range length C, and look their unit up in the running
+// count. If there are fewer tiles than half the CTAs that run at once, C makes one wave of equal ranges (a
+// single request's long cache: D = 256, one token over 25,000, took 27.7 us so and 39.5 in four waves).
+// Else it is the longest span divided by the f that an estimate of the time likes best (attn_time), a lane to
+// each: more ranges even out a batch's end, and each costs its CTA's beginning and end. A request's ranges
+// are of one length. The host sizes the grid by a bound; CTAs past the last unit leave.
 //
 // Partials. A tile seen in one range is finished by its unit. Otherwise every range leaves the running
 // maximum, the sum and the unnormalised output of its rows (32 bits) in a slot of the workspace,
@@ -44,6 +44,8 @@ struct AttnArgs {
     int align;         // ranges start at multiples of this many tokens (a power of two)
     int wave, target;  // units: CTAs that run at once, and of a batch (at least as many)
     int min_range;
+    int unit_cost, join_cost;  // of a unit's beginning and end, and of joining, in tokens of a CTA's work
+    bool soft;                 // memory-bound: a wave that is not full runs faster
 };
 
 struct AttnUnit {
@@ -85,6 +87,21 @@ __device__ __forceinline__ AttnRequest attn_request(const AttnArgs &a, int b) {
     return r;
 }
 
+// Estimated time, in tokens of one CTA, of tiles (with heads) of `all` tokens together and at most `longest` each,
+// cut into ranges of C.
+__device__ __forceinline__ float attn_time(const AttnArgs &a, float tiles, float all, float longest, float C) {
+    const float mean = __fdividef(all, tiles), wave = (float)a.wave, cost = (float)a.unit_cost;
+    const bool even = mean >= 0.9f * longest;
+    const float units = tiles * fmaxf(1.f, ceilf(even ? __fdividef(longest, C) - 1e-3f : __fdividef(mean, C) - 0.1f));
+    const float waves = __fdividef(units, wave);
+    float t;
+    if (a.soft) t = fmaxf(C, __fdividef(all, wave) + 0.5f * C) + cost * fmaxf(1.f, waves);
+    else if (waves <= 1.f) t = C + cost;
+    else if (even) t = ceilf(waves) * (C + cost);
+    else t = __fdividef(all, wave) + 0.5f * C + cost * waves;
+    return C < longest ? t + (float)a.join_cost : t;
+}
+
 // The unit with this number (JOIN: the tile and head with this number among those of requests with
 // several ranges), found by one warp; false if there is none.
 template <bool JOIN>
@@ -92,27 +109,41 @@ __device__ __forceinline__ bool attn_unit(const AttnArgs &a, int idx, AttnUnit &
     const int lane = threadIdx.x % 32, B = a.p.B, unit_log2 = 31 - __clz(a.align);
     AttnRequest r = {};
     long long work = 0;
-    int whole = 0;  // tiles
+    int whole = 0, longest = 0;  // tiles; the longest span
     if (B == 1) {   // (every lane has the one request: nothing to add up or to hand round)
         r = attn_request(a, 0);
         work = (long long)r.tiles * r.span;
         whole = r.tiles;
+        longest = r.span;
     } else {
         for (int i = 0; i < B; i += 32) {
             r = AttnRequest{};
             if (i + lane < B) r = attn_request(a, i + lane);
             work += (long long)r.tiles * r.span;
             whole += r.tiles;
+            longest = max(longest, r.tiles ? r.span : 0);
         }
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) work += __shfl_xor_sync(0xffffffffu, work, off);
         whole = __reduce_add_sync(0xffffffffu, whole);
+        longest = __reduce_max_sync(0xffffffffu, longest);
     }
-    const int target = 2 * (long long)whole * a.p.heads < a.wave ? a.wave : a.target;
-    // C = work * heads / target in units of align tokens (2^24 at most); 2^-20 less, so that what fits is not
-    // rounded up, which the slots' margin covers
-    const int C = (int)fminf(ceilf(__fdividef((float)work * (float)a.p.heads, (float)target * (float)a.align) * (1.f - 0x1p-20f)), 16777215.f);
-    const int least = a.min_range >> unit_log2, most = max(C, least);
+    // C in units of align tokens (2^24 at most), not below all / target, which bounds the units and slots; 2^-20 less,
+    // so that what fits is not rounded up, which the slots' margin covers
+    const float all = (float)work * (float)a.p.heads, tiles_all = (float)whole * (float)a.p.heads;
+    const bool few = 2 * (long long)whole * a.p.heads < a.wave;
+    auto at_least = [&](int units) {
+        return (int)fminf(ceilf(__fdividef(all, (float)units * (float)a.align) * (1.f - 0x1p-20f)), 16777215.f);
+    };
+    const int least = a.min_range >> unit_log2;
+    int most = max(at_least(few ? a.wave : a.target), least);
+    if (!few) {
+        const int units = (longest + a.align - 1) >> unit_log2, mine = attn_ceil_div(max(units, 1), lane + 1);
+        const float t = attn_time(a, tiles_all, all, (float)longest, (float)mine * (float)a.align);
+        // (the time in 27 bits, the lane in five: the fewest ranges of the best)
+        const unsigned key = (mine >= most || lane == 0 ? (unsigned)fminf(t, 67108863.f) << 5 : 0xffffffe0u) | lane;
+        most = max(__shfl_sync(0xffffffffu, mine, __reduce_min_sync(0xffffffffu, key) & 31), least);
+    }
     // equal ranges of at most `most`
     auto cut = [&](int span, int &step) {
         const int units = (span + a.align - 1) >> unit_log2;

@@ -155,6 +155,8 @@ struct TileShape {
     static constexpr bool TWICE = KV8 && D == 128;
     static constexpr int THREADS = SOFTMAX + 128 + 2 * CVT;
     static_assert(THREADS % 128 == 0, "register splits go by warpgroups");
+    // 256 columns of a row are more than four warps write in a hurry (8 bits: the registers are worth more elsewhere)
+    static constexpr bool BOTH = NS == 1 && !KV8;
     // columns of tensor memory: S at 0 and BN, P in the place of S for D = 128 (where that fills the
     // 512 columns), else beside it
     static constexpr int COL_P = D == 128 ? 0 : D == 64 ? 384 : 128, P_STEP = D == 128 ? BN : BN / 2, COL_O = 256, O_STEP = D;
@@ -167,13 +169,15 @@ struct TileShape {
     static constexpr int OFF_RAW = OFF_RING + SLOTS * TILE;
     static constexpr int OFF_POW = OFF_RAW + RAWS * RAW;  // [2][4][BN]: powers of two of a key or value tile's tokens
     static constexpr int OFF_BAR = OFF_POW + (KV8 ? 2 * 4 * BN * 4 : 0);
-    static constexpr int BYTES = OFF_BAR + 1024 + 1024;                        // and the alignment of the base
+    static constexpr int BYTES = OFF_BAR + 2048 + 1024;                        // and the alignment of the base
     static_assert(BYTES <= 232448, "shared memory of one CTA");
     // Barriers go by tile modulo 4, so a tile's copy must not be issued before the tile four earlier has been
     // used: key tile 4 is the eighth copy of a ring (see seq_k), tile 0 the first.
     static_assert(SLOTS + (NS == 2) <= 7 && RAWS <= 7, "a ring holds fewer copies than lie between tiles t and t + 4");
     static_assert(NS == 1 || QTILE == TILE, "a q tile's place is a slot");
-    static_assert(NS == 1 || 8192 + 128 * (D + 4) * 4 + 1024 <= SLOTS * TILE, "the streams merge in the ring");
+    static constexpr int STAGE = 32 * ((KV8 || D == 64 ? 32 : 64) + 4) * 4;  // a warp's rows on their way out, from the first byte
+    static_assert(NS == 1 || 8 * STAGE <= OFF_RING + 8192, "rows on their way out lie before the merge");
+    static_assert(NS == 1 || 8192 + 2 * 128 * (D / 2 + 4) * 4 + 2048 <= SLOTS * TILE, "the streams merge in the ring");
 };
 
 struct Bars {
@@ -181,9 +185,16 @@ struct Bars {
     unsigned long long full[2][4], empty[2][4], raw_full[2][4], raw_empty[2][4], pow_full[2][4], ref_full[4], s_full[2], p_full[2], pv, q_full, q_ready, last_v, fin;
     uint32_t tmem;
     int abort, k_ref[4], v_ref[4];
-    signed char q_exp[256];  // powers of two of bf16 q rows brought to fp16
+    AttnUnit unit[8];  // the unit again, for the end (a copy a warp: held in registers it would cost the softmax some)
+    union {
+        signed char q_exp[256];  // powers of two of bf16 q rows brought to fp16 (at the start)
+        struct {                 // D = 256: the rows' factors and places, for the warps that write half of the columns (at the end)
+            float row_f[128];
+            int row_at[128];
+        };
+    };
 };
-static_assert(sizeof(Bars) <= 1024, "barriers");
+static_assert(sizeof(Bars) <= 2048, "barriers");
 
 // Place of K (or V) tile t of n in the ring's order, and the other way round.
 __device__ __forceinline__ int seq_k(bool two_q, int t) { return two_q ? 2 * t : (t == 0 ? 0 : 2 * t - 1); }
@@ -195,6 +206,68 @@ __device__ __forceinline__ void seq_tile(bool two_q, int seq, int n, int &t, boo
     } else {
         is_v = seq == 2 * n - 1 || (seq > 0 && !(seq & 1));
         t = seq == 2 * n - 1 ? n - 1 : (seq & 1) ? (seq + 1) >> 1 : seq == 0 ? 0 : (seq - 2) >> 1;
+    }
+}
+
+// A copy from shared memory that is not what the compiler still holds in registers.
+__device__ __forceinline__ AttnUnit again(AttnUnit &from) {
+    AttnUnit u;
+    int *to = reinterpret_cast<int *>(&u);
+    const volatile int *at = reinterpret_cast<const volatile int *>(&from);
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(AttnUnit) / 4); ++i) to[i] = at[i];
+    return u;
+}
+
+// One warp's 32 rows (lane: row) x `cols` columns of an accumulator, times f0, plus f1 times `other` (the row's
+// values in shared memory, or null), to out (part null) or to a slot of the workspace; `at` is the row of out,
+// -1 where there is none. EC columns at a time pass through shared memory, so that EC / 4 lanes write a row's
+// neighbouring columns: a lane writing its own row would touch 32 lines a store. Tensor-memory loads are the
+// whole warp's, whatever its rows.
+template <int D, bool KV8>
+__device__ __forceinline__ void put_rows(const AttnArgs &a, void *shared, uint32_t addr, int c0, int cols, float f0, bool any, float f1,
+                                         const float *other, float *part, int row0, int at, bool bf) {
+    constexpr int EC = KV8 || D == 64 ? 32 : 64, ER = 128 / EC;  // columns at a time, rows a store
+    const int lane = threadIdx.x % 32;
+    if (!__any_sync(0xffffffffu, at >= 0)) return;
+    float *stage = static_cast<float *>(shared);
+#pragma unroll 1
+    for (int d = 0; d < cols; d += EC) {
+        uint32_t y[EC / 32][32];
+        if (any) {
+#pragma unroll
+            for (int i = 0; i < EC / 32; ++i) tmem_ld32_start(addr + d + 32 * i, y[i]);
+            tmem_wait_ld(y);
+        }
+#pragma unroll
+        for (int e = 0; e < EC; e += 4) {
+            float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (any)
+                z = make_float4(f0 * __uint_as_float(y[e / 32][e % 32]), f0 * __uint_as_float(y[e / 32][e % 32 + 1]),
+                                f0 * __uint_as_float(y[e / 32][e % 32 + 2]), f0 * __uint_as_float(y[e / 32][e % 32 + 3]));
+            if (other) {
+                const float4 w = *reinterpret_cast<const float4 *>(other + d + e);
+                z = make_float4(fmaf(f1, w.x, z.x), fmaf(f1, w.y, z.y), fmaf(f1, w.z, z.z), fmaf(f1, w.w, z.w));
+            }
+            *reinterpret_cast<float4 *>(stage + lane * (EC + 4) + e) = z;
+        }
+        __syncwarp();
+#pragma unroll 8
+        for (int i = 0; i < 32 / ER; ++i) {
+            const int r = ER * i + lane / (EC / 4), e = 4 * (lane % (EC / 4));
+            const int row_at = __shfl_sync(0xffffffffu, at, r);
+            const float4 w = *reinterpret_cast<const float4 *>(stage + r * (EC + 4) + e);
+            if (row_at < 0) continue;
+            if (!part) {
+                uint2 h;
+                h.x = bf ? pack2<true>(w.x, w.y) : pack2<false>(w.x, w.y);
+                h.y = bf ? pack2<true>(w.z, w.w) : pack2<false>(w.z, w.w);
+                *reinterpret_cast<uint2 *>(static_cast<unsigned short *>(a.out) + (size_t)row_at * D + c0 + d + e) = h;
+            } else {
+                *reinterpret_cast<float4 *>(part + (size_t)(row0 + r) * D + c0 + d + e) = w;
+            }
+        }
+        __syncwarp();
     }
 }
 
@@ -233,11 +306,22 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_proxy_async();
     }
+    if (warp == W_MMA) tmem_alloc<512>(&bar.tmem);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tm = bar.tmem;
+    volatile int *abort = &bar.abort;
+    // (all of this beside the launch before; from here on every warp goes its own way)
     grid_dep_wait();
     grid_dep_trigger();
     AttnUnit u;
-    if (!attn_unit<false>(a, blockIdx.x, u)) return;
-    if (u.c >= u.ranges) return;
+    if (!attn_unit<false>(a, blockIdx.x, u) || u.c >= u.ranges) {
+        if (warp == W_MMA) tmem_free<512>(tm);
+        return;
+    }
+    if (warp < 8 && lane == 0) bar.unit[warp] = u;
+    __syncwarp();
     const int mq_rows = a.M / NS;                                 // rows of a q tile: whole tokens, at most 128
     const int row0 = u.t * a.M, rows = min(a.M, u.n * a.G - row0);  // (the host bounds total * heads)
     const bool two_q = NS == 2 && rows > mq_rows;
@@ -248,13 +332,6 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
     unsigned char *ring = smem + S::OFF_RING - (wide ? S::QTILE : 0);
     const int slots = wide ? SLOTS + 1 : SLOTS;
     auto slot_of = [&](int seq) { return wide ? seq % (SLOTS + 1) : seq % SLOTS; };
-
-    if (warp == W_MMA) tmem_alloc<512>(&bar.tmem);
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tm = bar.tmem;
-    volatile int *abort = &bar.abort;
 
     if (warp == W_TMA || (!KV8 && warp == W_TMA + 3)) {
         if (S::SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::R_OTHER));
@@ -650,103 +727,76 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             tc_fence_before();
             mbar_arrive(&bar.p_full[j & 1]);
         }
-        // ---- the outputs (tensor-memory loads are the whole warp's, stores each row's own)
+        // ---- the outputs
         if (steps > 0 && ok) ok = wait_for(&bar.fin, 0, abort);
         tc_fence_after();
         const float unit = KV8 ? ex2((float)(ref - 127)) : 1.f;
-        constexpr int PITCH = D + 4;
+        const AttnUnit v = again(bar.unit[warp]);
+        const int first = v.t * a.M, r_here = (NS == 2 && two_q ? s * mq_rows : 0) + row;
+        const bool merge = NS == 2 && !two_q, final = v.ranges == 1;
+        constexpr int HALF = D / 2, PITCH = HALF + 4;
+        // two streams of the same rows: each hands the other half of its columns, and finishes the rest
         unsigned char *mine = smem + S::OFF_RING + 8192;  // (rows on their way out may take the bytes before)
-        float *mo = reinterpret_cast<float *>(mine);
-        float2 *ml = reinterpret_cast<float2 *>(mine + 128 * PITCH * 4);
-        const bool merge = NS == 2 && !two_q;
+        float *to = reinterpret_cast<float *>(mine) + s * 128 * PITCH, *from = reinterpret_cast<float *>(mine) + (1 - s) * 128 * PITCH;
+        float2 *ml = reinterpret_cast<float2 *>(mine + 2 * 128 * PITCH * 4);
+        float top = m, f0 = unit, f1 = 0.f, sum = l;
         if (merge) {
-            if (ok && s == 1) {
-                ml[row] = make_float2(m, l);
+            ml[s * 128 + row] = make_float2(m, l);
 #pragma unroll 1
-                for (int d = 0; any && d < D; d += 32) {
-                    uint32_t y[1][32];
-                    tmem_ld32_start(o_addr + d, y[0]);
-                    tmem_wait_ld(y);
+            for (int d = 0; ok && any && d < HALF; d += 32) {
+                uint32_t y[1][32];
+                tmem_ld32_start(o_addr + (1 - s) * HALF + d, y[0]);
+                tmem_wait_ld(y);
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<float4 *>(mo + row * PITCH + d + e) =
-                            make_float4(__uint_as_float(y[0][e]) * unit, __uint_as_float(y[0][e + 1]) * unit,
-                                        __uint_as_float(y[0][e + 2]) * unit, __uint_as_float(y[0][e + 3]) * unit);
-                }
+                for (int e = 0; e < 32; e += 4)
+                    *reinterpret_cast<float4 *>(to + row * PITCH + d + e) =
+                        make_float4(__uint_as_float(y[0][e]) * unit, __uint_as_float(y[0][e + 1]) * unit,
+                                    __uint_as_float(y[0][e + 2]) * unit, __uint_as_float(y[0][e + 3]) * unit);
             }
             bar_sync(2, 256);
+            const float2 y = ml[(1 - s) * 128 + row];
+            top = fmaxf(m, y.x);
+            const float base = top == -INFINITY ? 0.f : top;
+            f0 = ex2(m - base);
+            f1 = ex2(y.x - base);
+            sum = s ? f1 * y.y + f0 * l : f0 * l + f1 * y.y;
+            f0 *= unit;
         }
-        if (ok && !(merge && s == 1) && __any_sync(0xffffffffu, row < mq_rows && r_unit < rows)) {
-            const bool other = merge && tiles > 1;  // (stream 1 has a tile of its own)
-            float top = m, f0 = unit, f1 = 0.f, sum = l;
-            if (other) {
-                const float2 y = ml[row];
-                top = fmaxf(m, y.x);
-                const float base = top == -INFINITY ? 0.f : top;
-                f0 = ex2(m - base);
-                f1 = ex2(y.x - base);
-                sum = f0 * l + f1 * y.y;
-                f0 *= unit;
-            }
-            const bool final = u.ranges == 1;
-            if (final) {
-                const float inv = sum > 0.f ? 1.f / sum : sum != sum ? sum : 0.f;  // NaN stays NaN
-                f0 *= inv;
-                f1 *= inv;
-            }
-            // row of out and lse; a slot's rows are dense
-            const int at = (u.s + tok) * (a.p.heads * a.G) + u.h * a.G + (row0 + r_unit - tok * a.G);
-            float *part = a.part + (size_t)(u.slot + u.c) * a.M * (D + 2);
-            const bool bf = KV8 ? io_bf : BF;
-            // A warp's 32 rows x EC columns pass through shared memory (the q tiles' place), so that EC / 4 lanes
-            // write a row's neighbouring columns; a lane writing its own row would touch 32 lines a store.
-            constexpr int EC = KV8 ? 32 : 64, ER = 128 / EC;  // columns at a time, rows a store
-            float *stage = reinterpret_cast<float *>(smem) + warp * (32 * (EC + 4));
-#pragma unroll 1
-            for (int d = 0; d < D; d += EC) {
-                uint32_t y[EC / 32][32];
-                if (any) {
-#pragma unroll
-                    for (int i = 0; i < EC / 32; ++i) tmem_ld32_start(o_addr + d + 32 * i, y[i]);
-                    tmem_wait_ld(y);
-                }
-#pragma unroll
-                for (int e = 0; e < EC; e += 4) {
-                    float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (any)
-                        z = make_float4(f0 * __uint_as_float(y[e / 32][e % 32]), f0 * __uint_as_float(y[e / 32][e % 32 + 1]),
-                                        f0 * __uint_as_float(y[e / 32][e % 32 + 2]), f0 * __uint_as_float(y[e / 32][e % 32 + 3]));
-                    if (other) {
-                        const float4 w = *reinterpret_cast<const float4 *>(mo + row * PITCH + d + e);
-                        z = make_float4(fmaf(f1, w.x, z.x), fmaf(f1, w.y, z.y), fmaf(f1, w.z, z.z), fmaf(f1, w.w, z.w));
-                    }
-                    *reinterpret_cast<float4 *>(stage + lane * (EC + 4) + e) = z;
-                }
-                __syncwarp();
-#pragma unroll 8
-                for (int i = 0; i < 32 / ER; ++i) {
-                    const int r = ER * i + lane / (EC / 4), e = 4 * (lane % (EC / 4)), ru = r_unit - lane + r;
-                    const int row_at = __shfl_sync(0xffffffffu, at, r), r_tile = row - lane + r;
-                    const float4 w = *reinterpret_cast<const float4 *>(stage + r * (EC + 4) + e);
-                    if (r_tile >= mq_rows || ru >= rows) continue;
-                    if (final) {
-                        uint2 h;
-                        h.x = bf ? pack2<true>(w.x, w.y) : pack2<false>(w.x, w.y);
-                        h.y = bf ? pack2<true>(w.z, w.w) : pack2<false>(w.z, w.w);
-                        *reinterpret_cast<uint2 *>(static_cast<unsigned short *>(a.out) + (size_t)row_at * D + d + e) = h;
-                    } else {
-                        *reinterpret_cast<float4 *>(part + (size_t)ru * D + d + e) = w;
-                    }
-                }
-                __syncwarp();
-            }
-            const bool live = row < mq_rows && r_unit < rows;
-            if (live && final) {
-                if (a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945f;
-            } else if (live) {
-                *reinterpret_cast<float2 *>(part + (size_t)a.M * D + 2 * r_unit) = make_float2(top, sum);
-            }
+        if (final) {
+            const float inv = sum > 0.f ? 1.f / sum : sum != sum ? sum : 0.f;  // NaN stays NaN
+            f0 *= inv;
+            f1 *= inv;
         }
+        // the row's place in out and lse; a slot's rows are dense
+        const bool live = row < mq_rows && r_here < v.n * a.G - first;
+        const int token = (first + r_here) / a.G, at = (v.s + token) * (a.p.heads * a.G) + v.h * a.G + (first + r_here - token * a.G);
+        float *part = a.part + (size_t)(v.slot + v.c) * a.M * (D + 2);
+        if (ok && live && !(merge && s == 1)) {
+            if (!final) *reinterpret_cast<float2 *>(part + (size_t)a.M * D + 2 * r_here) = make_float2(top, sum);
+            else if (a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945f;
+        }
+        if (S::BOTH) {  // the other four warps write half of the columns
+            bar.row_f[row] = ok && any ? f0 : 0.f;
+            bar.row_at[row] = live && ok ? at : -1;
+            tc_fence_before();
+            bar_sync(2, 256);
+        }
+        const int c0 = merge ? s * HALF : 0;
+        const bool other = merge && (s ? tiles > 0 : tiles > 1);
+        if (ok)
+            put_rows<D, KV8>(a, smem + warp * S::STAGE, o_addr + c0, c0, S::BOTH || merge ? HALF : D, f0, any, f1, other ? from + row * PITCH : nullptr,
+                             final ? nullptr : part, r_here - lane, live ? at : -1, KV8 ? io_bf : BF);
+        tc_fence_before();
+    }
+    if (S::BOTH && warp >= W_TMA && warp < W_TMA + 4) {
+        // ---- the second half of a 256-wide output
+        bar_sync(2, 256);
+        tc_fence_after();
+        const int row = 32 * (warp % 4) + lane, at = bar.row_at[row];
+        const AttnUnit v = again(bar.unit[warp]);
+        float *part = a.part + (size_t)(v.slot + v.c) * a.M * (D + 2);
+        put_rows<D, KV8>(a, smem + warp * S::STAGE, tm + ((uint32_t)(32 * (warp % 4)) << 16) + S::COL_O + D / 2, D / 2, D / 2, bar.row_f[row],
+                         steps > 0, 0.f, nullptr, v.ranges == 1 ? nullptr : part, row - lane, at, KV8 ? io_bf : BF);
         tc_fence_before();
     }
     __syncthreads();
