@@ -624,7 +624,7 @@ extern "C" dn_status dn_attn_paged(int B, int total, int heads_kv, int group, in
                                    void *workspace, size_t workspace_bytes, dn_stream_t stream) {
     using namespace dn;
     if (B < 0 || total < 0 || total > DN_KV_MAX_ROWS || heads_kv < 1 || group < 1 || window < 0 ||
-        !(scale > 0.f) || scale > 3e38f || !kv_dtypes_known(io_dt, cache_dt))
+        !(scale > 0.f) || !(scale < 2e38f) || !kv_dtypes_known(io_dt, cache_dt))
         return DN_ERR_INVALID_ARG;
     if (!kv_shape_ok(D, page) || !kv_dtypes_ok(io_dt, cache_dt)) return DN_ERR_UNSUPPORTED;
     if ((long long)heads_kv * group > (1 << 20) || (long long)total * heads_kv * group > 0x7fffffffLL - 1024 ||

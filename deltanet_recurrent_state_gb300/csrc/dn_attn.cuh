@@ -130,7 +130,8 @@ __device__ __forceinline__ bool attn_unit(const AttnArgs &a, int idx, AttnUnit &
     }
     // C in units of align tokens (2^24 at most), not below all / target, which bounds the units and slots; 2^-20 less,
     // so that what fits is not rounded up, which the slots' margin covers
-    const float all = (float)work * (float)a.p.heads, tiles_all = (float)whole * (float)a.p.heads;
+    // (a 64-bit integer to float goes through the fp64 pipe, so it goes in two parts)
+    const float all = ((float)(int)(work >> 24) * 16777216.f + (float)(int)(work & 0xffffff)) * (float)a.p.heads, tiles_all = (float)whole * (float)a.p.heads;
     const bool few = 2 * (long long)whole * a.p.heads < a.wave;
     auto at_least = [&](int units) {
         return (int)fminf(ceilf(__fdividef(all, (float)units * (float)a.align) * (1.f - 0x1p-20f)), 16777215.f);

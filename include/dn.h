@@ -471,7 +471,7 @@ dn_status dn_kv_gather(int B, int total, int heads, int D, int page, int max_pag
  *   heads_kv, group  key heads, and query heads of each (heads_kv * group query heads)
  *   q         row t at q + t * q_stride elements, [heads_kv * group][D] dense inside; io_dt, 16-byte
  *             aligned, q_stride a multiple of 8 and >= heads_kv * group * D
- *   scale     > 0, finite;  window  tokens that a row looks back, itself included; 0: all
+ *   scale     > 0 and < 2e38;  window  tokens that a row looks back, itself included; 0: all
  *   out       [total][heads_kv * group][D] io_dt, dense, 16-byte aligned, written
  *   lse       [total][heads_kv * group] fp32, written, or NULL
  *   workspace >= dn_attn_workspace_bytes(...) bytes, 16-byte aligned, any contents; calls that may
