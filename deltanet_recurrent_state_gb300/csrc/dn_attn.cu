@@ -28,6 +28,7 @@
 #include "dn.h"
 #include "dn_attn.cuh"
 #include "dn_internal.h"
+#include "dn_kv_host.h"
 #include "dn_mma.cuh"
 
 namespace dn {

@@ -16,6 +16,7 @@
 #include "dn_device.cuh"
 #include "dn_internal.h"
 #include "dn_kv.cuh"
+#include "dn_kv_host.h"
 
 namespace dn {
 namespace {
