@@ -50,12 +50,8 @@ def quantise(x):
     x = np.asarray(x, dtype=np.float64)
     big = np.max(np.where(np.isnan(x), 0.0, np.abs(x)), axis=-1)
     E = np.zeros(big.shape, dtype=np.uint8)
-    for i in np.ndindex(big.shape):
-        if big[i] > 0:
-            e = -127
-            while e < 127 and big[i] > 448.0 * 2.0 ** e:
-                e += 1
-            E[i] = e + 127
+    for e in range(-127, 127):  # one more for every power of two that does not hold the row
+        E += big > 448.0 * 2.0 ** e
     return encode_e4m3(np.clip(x * 2.0 ** (127.0 - E[..., None]), -448, 448)), E
 
 
