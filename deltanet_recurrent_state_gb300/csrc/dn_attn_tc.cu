@@ -11,7 +11,8 @@
 // even and the odd steps are two streams with a warpgroup and an accumulator each: if the unit has more
 // than 128 rows (a prompt's chunk) the streams are its two halves of rows over the same keys, else
 // (a verify block) they are the even and the odd key tiles of the same rows, merged at the end. For D = 256
-// an accumulator takes half of the tensor memory: one stream, key tiles of 64 tokens.
+// an accumulator takes half of the tensor memory: one stream, key tiles of 64 tokens, of which each of the two
+// warpgroups has half of the columns.
 //
 // Copies. K and V tiles pass through one ring of shared-memory slots in the order in which the products take
 // them. Pages come in by TMA, one box per page and 64 columns, with the 128-byte swizzle that the MMA
@@ -142,34 +143,34 @@ struct TileShape {
     static constexpr int HALVES = D / 64;            // 64-column boxes of a tile
     static constexpr int TILE = BN * D * 2;          // bytes of a 16-bit K or V tile
     static constexpr int QTILE = 128 * D * 2;
-    static constexpr int SLOTS = KV8 ? (D == 64 ? 4 : 3) : (D == 64 ? 6 : 5);
+    static constexpr int SLOTS = KV8 ? (D == 64 ? 4 : 3) : (D == 64 ? 6 : D == 128 ? 5 : 4);
     static constexpr int RAW = KV8 ? BN * D : 0;     // bytes of an 8-bit tile
     static constexpr int RAWS = KV8 ? (D == 64 ? 4 : 3) : 0;
-    static constexpr int SOFTMAX = 128 * NS;         // threads of the softmax warpgroups
+    static constexpr int SOFTMAX = 256;              // threads of the softmax warpgroups: a row each, or half a row (D = 256)
+    static constexpr int CN = BN * NS / 2;           // columns of S that a thread has
     // Threads that turn 8-bit tiles into fp16: one group for the keys and one for the values, so that one's
     // waits pass beside the other's work. The more elements a token has, the more of the block's registers
     // they are worth: for D = 64 the softmax keeps its scores in registers (three prompts' window of 1,000 took
     // 88 us so, and 104 with 14 such warps), for D = 128 it reads them twice (32 verify blocks of 64 rows: 256 us
     // with 14 warps, 328 with 6).
-    static constexpr int CVT = KV8 ? (D == 64 ? 64 : D == 128 ? 192 : 256) : 0;
+    static constexpr int CVT = KV8 ? (D == 64 ? 64 : 192) : 0;
     static constexpr bool TWICE = KV8 && D == 128;
     static constexpr int THREADS = SOFTMAX + 128 + 2 * CVT;
     static_assert(THREADS % 128 == 0, "register splits go by warpgroups");
-    // 256 columns of a row are more than four warps write in a hurry (8 bits: the registers are worth more elsewhere)
-    static constexpr bool BOTH = NS == 1 && !KV8;
     // columns of tensor memory: S at 0 and BN, P in the place of S for D = 128 (where that fills the
     // 512 columns), else beside it
     static constexpr int COL_P = D == 128 ? 0 : D == 64 ? 384 : 128, P_STEP = D == 128 ? BN : BN / 2, COL_O = 256, O_STEP = D;
     // registers of a softmax thread and of the others; the sum stays within the launch's
     static constexpr bool SPLIT = NS == 2 || KV8;
-    static constexpr int R_SOFTMAX = !KV8 ? 208 : D == 64 ? 176 : 112, R_OTHER = !KV8 ? 88 : D == 64 ? 80 : D == 128 ? 64 : 72;
+    static constexpr int R_SOFTMAX = !KV8 ? 208 : D == 64 ? 176 : D == 128 ? 112 : 96, R_OTHER = !KV8 ? 88 : D == 64 ? 80 : D == 128 ? 64 : 72;
     static constexpr int R_LAUNCH = 65536 / THREADS / 8 * 8;
     static_assert(!SPLIT || SOFTMAX * R_SOFTMAX + (THREADS - SOFTMAX) * R_OTHER <= THREADS * R_LAUNCH, "registers");
     static constexpr int OFF_RING = NS * QTILE;
     static constexpr int OFF_RAW = OFF_RING + SLOTS * TILE;
     static constexpr int OFF_POW = OFF_RAW + RAWS * RAW;  // [2][4][BN]: powers of two of a key or value tile's tokens
     static constexpr int OFF_BAR = OFF_POW + (KV8 ? 2 * 4 * BN * 4 : 0);
-    static constexpr int BYTES = OFF_BAR + 2048 + 1024;                        // and the alignment of the base
+    static constexpr int OFF_ROW = OFF_BAR + 2048;  // D = 256: [2][2][128] maxima of half rows, [2][128] their sums
+    static constexpr int BYTES = OFF_ROW + (NS == 1 ? 3072 : 0) + 1024;                        // and the alignment of the base
     static_assert(BYTES <= 232448, "shared memory of one CTA");
     // Barriers go by tile modulo 4, so a tile's copy must not be issued before the tile four earlier has been
     // used: key tile 4 is the eighth copy of a ring (see seq_k), tile 0 the first.
@@ -182,17 +183,11 @@ struct TileShape {
 
 struct Bars {
     // by kind (keys, values) and tile modulo 4
-    unsigned long long full[2][4], empty[2][4], raw_full[2][4], raw_empty[2][4], pow_full[2][4], ref_full[4], s_full[2], p_full[2], pv, q_full, q_ready, last_v, fin;
+    unsigned long long full[2][4], empty[2][4], raw_full[2][4], raw_empty[2][4], pow_full[2][4], ref_full[4], s_full[2], p_full[2], most_full[2], pv, q_full, q_ready, last_v, fin;
     uint32_t tmem;
     int abort, k_ref[4], v_ref[4];
     AttnUnit unit[8];  // the unit again, for the end (a copy a warp: held in registers it would cost the softmax some)
-    union {
-        signed char q_exp[256];  // powers of two of bf16 q rows brought to fp16 (at the start)
-        struct {                 // D = 256: the rows' factors and places, for the warps that write half of the columns (at the end)
-            float row_f[128];
-            int row_at[128];
-        };
-    };
+    signed char q_exp[256];  // powers of two of bf16 q rows brought to fp16
 };
 static_assert(sizeof(Bars) <= 2048, "barriers");
 
@@ -276,13 +271,14 @@ __global__ void __launch_bounds__(TileShape<D, KV8>::THREADS, 1)
 attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUtensorMap mq,
                  const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, bool io_bf) {
     using S = TileShape<D, KV8>;
-    constexpr int BN = S::BN, NS = S::NS, SLOTS = S::SLOTS, TILE = S::TILE;
+    constexpr int BN = S::BN, CN = S::CN, NS = S::NS, SLOTS = S::SLOTS, TILE = S::TILE;
     constexpr bool MB = BF && !KV8;
     constexpr int W_TMA = S::SOFTMAX / 32, W_MMA = W_TMA + 1;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *smem = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     unsigned char *raw = smem + S::OFF_RAW;
     Bars &bar = *reinterpret_cast<Bars *>(smem + S::OFF_BAR);
+    float *row_most = reinterpret_cast<float *>(smem + S::OFF_ROW), *row_sum = row_most + 512;  // (D = 256)
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     if (tid == 0) {
         for (int i = 0; i < 8; ++i) {
@@ -295,7 +291,8 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
         for (int i = 0; i < 4; ++i) mbar_init(&bar.ref_full[i], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar.s_full[i], 1);
-            mbar_init(&bar.p_full[i], 128);
+            mbar_init(&bar.p_full[i], NS == 1 ? 256 : 128);
+            mbar_init(&bar.most_full[i], 256);
         }
         mbar_init(&bar.pv, 1);
         mbar_init(&bar.q_full, 1);
@@ -564,7 +561,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             mbar_arrive(&bar.raw_empty[is_v][t & 3]);
         }
     } else {
-        // ---- softmax: a thread per row
+        // ---- softmax: a thread per row, or (D = 256, one stream) two threads with half of its columns each
         if (S::SPLIT) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::R_SOFTMAX));
         const int s = warp / 4, row = tid % 128;
         const int r_unit = two_q ? s * mq_rows + row : row;  // this thread's row of the unit
@@ -622,10 +619,10 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
         int ref = 0;
         for (int j = NS == 2 ? s : 0; ok && j < steps; j += NS) {
             const int t = two_q ? j >> 1 : j, j0 = u.lo + t * BN;
-            const uint32_t s_addr = tm + lanes + (j & 1) * BN, p_addr = tm + lanes + S::COL_P + (j & 1) * S::P_STEP;
+            const uint32_t s_addr = tm + lanes + (j & 1) * BN + (NS == 1 ? s * CN : 0), p_addr = tm + lanes + S::COL_P + (j & 1) * S::P_STEP + (NS == 1 ? s * CN / 2 : 0);
             if (!wait_for(&bar.s_full[j & 1], (j >> 1) & 1, abort)) { ok = false; break; }
             tc_fence_after();
-            constexpr int HELD = S::TWICE ? 2 : BN / 32;  // groups of 32 columns held in registers
+            constexpr int HELD = S::TWICE ? 2 : CN / 32;  // groups of 32 columns held in registers
             uint32_t x[HELD][32];
 #pragma unroll
             for (int i = 0; i < HELD; ++i) tmem_ld32_start(s_addr + 32 * i, x[i]);
@@ -640,7 +637,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             if (!ok) break;
             // columns least < i <= most are seen, as bits of each 32
             const bool edge = j0 + BN - 1 > pos_first || j0 + BN > u.hi || (a.window && j0 <= pos_last - a.window);
-            const int most = min(pos, u.hi - 1) - j0, least = a.window ? pos - a.window - j0 : -1;
+            const int c0 = NS == 1 ? s * CN : 0, most = min(pos, u.hi - 1) - j0 - c0, least = a.window ? pos - a.window - j0 - c0 : -1 - c0;
             auto hide = [&](uint32_t(&y)[32], int i) {
                 const int up = most - 32 * i, down = least - 32 * i;
                 const unsigned keep = (up >= 31 ? 0xffffffffu : up < 0 ? 0u : (2u << up) - 1u) &
@@ -650,7 +647,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             };
             float b[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int i0 = 0; i0 < BN / 32; i0 += HELD) {
+            for (int i0 = 0; i0 < CN / 32; i0 += HELD) {
                 if (i0 > 0) {
 #pragma unroll
                     for (int i = 0; i < HELD; ++i) tmem_ld32_start(s_addr + 32 * (i0 + i), x[i]);
@@ -666,7 +663,13 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                     for (int e = 0; e < 4; ++e)
                         b[e] = fmaxf(fmaxf(b[e], __uint_as_float(x[i / 32][i % 32 + 2 * e])), __uint_as_float(x[i / 32][i % 32 + 2 * e + 1]));
             }
-            const float big = fmaxf(fmaxf(b[0], b[1]), fmaxf(b[2], b[3])) * factor;
+            float big = fmaxf(fmaxf(b[0], b[1]), fmaxf(b[2], b[3])) * factor;
+            if (NS == 1) {  // with the other half of the row's columns
+                row_most[((j & 1) * 2 + s) * 128 + row] = big;
+                mbar_arrive(&bar.most_full[j & 1]);
+                if (!wait_for(&bar.most_full[j & 1], (j >> 1) & 1, abort)) { ok = false; break; }
+                big = fmaxf(big, row_most[((j & 1) * 2 + 1 - s) * 128 + row]);
+            }
             if (!any) {
                 any = true;
                 m = big;
@@ -686,7 +689,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                         tc_fence_after();
                     }
 #pragma unroll 1
-                    for (int d = 0; d < D; d += 32) {
+                    for (int d = NS == 1 ? s * (D / 2) : 0; d < (NS == 1 ? (s + 1) * (D / 2) : D); d += 32) {
                         uint32_t y[1][32];
                         tmem_ld32_start(o_addr + d, y[0]);
                         tmem_wait_ld(y);
@@ -699,16 +702,16 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             const float base = m == -INFINITY ? 0.f : m;
             const float2 f2 = make_float2(factor, factor), b2 = make_float2(-base, -base);
             float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            if (HELD < BN / 32) {
+            if (HELD < CN / 32) {
                 uint32_t(&y)[1][32] = reinterpret_cast<uint32_t(&)[1][32]>(x[0]);
                 tmem_ld32_start(s_addr, x[0]);
                 tmem_wait_ld(y);
                 if (edge) hide(x[0], 0);
             }
 #pragma unroll
-            for (int i = 0; i < BN / 32; ++i) {
-                uint32_t p[16], (&now)[32] = x[HELD < BN / 32 ? i & 1 : i], (&next)[32] = x[HELD < BN / 32 ? (i + 1) & 1 : 0];
-                if (HELD < BN / 32 && i + 1 < BN / 32) tmem_ld32_start(s_addr + 32 * (i + 1), next);
+            for (int i = 0; i < CN / 32; ++i) {
+                uint32_t p[16], (&now)[32] = x[HELD < CN / 32 ? i & 1 : i], (&next)[32] = x[HELD < CN / 32 ? (i + 1) & 1 : 0];
+                if (HELD < CN / 32 && i + 1 < CN / 32) tmem_ld32_start(s_addr + 32 * (i + 1), next);
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
                     float2 y = __ffma2_rn(make_float2(__uint_as_float(now[e]), __uint_as_float(now[e + 1])), f2, b2);
@@ -716,7 +719,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                     l2[(e >> 1) & 1] = __fadd2_rn(l2[(e >> 1) & 1], y);
                     p[e / 2] = pack2<MB>(y.x, y.y);
                 }
-                if (HELD < BN / 32 && i + 1 < BN / 32) {
+                if (HELD < CN / 32 && i + 1 < CN / 32) {
                     tmem_wait_ld(reinterpret_cast<uint32_t(&)[1][32]>(next));
                     if (edge) hide(next, i + 1);
                 }
@@ -740,6 +743,11 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
         float *to = reinterpret_cast<float *>(mine) + s * 128 * PITCH, *from = reinterpret_cast<float *>(mine) + (1 - s) * 128 * PITCH;
         float2 *ml = reinterpret_cast<float2 *>(mine + 2 * 128 * PITCH * 4);
         float top = m, f0 = unit, f1 = 0.f, sum = l;
+        if (NS == 1) {  // the sum of the other half of the columns
+            row_sum[s * 128 + row] = l;
+            bar_sync(2, 256);
+            sum = row_sum[row] + row_sum[128 + row];
+        }
         if (merge) {
             ml[s * 128 + row] = make_float2(m, l);
 #pragma unroll 1
@@ -771,32 +779,15 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
         const bool live = row < mq_rows && r_here < v.n * a.G - first;
         const int token = (first + r_here) / a.G, at = (v.s + token) * (a.p.heads * a.G) + v.h * a.G + (first + r_here - token * a.G);
         float *part = a.part + (size_t)(v.slot + v.c) * a.M * (D + 2);
-        if (ok && live && !(merge && s == 1)) {
+        if (ok && live && !((merge || NS == 1) && s == 1)) {
             if (!final) *reinterpret_cast<float2 *>(part + (size_t)a.M * D + 2 * r_here) = make_float2(top, sum);
             else if (a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945f;
         }
-        if (S::BOTH) {  // the other four warps write half of the columns
-            bar.row_f[row] = ok && any ? f0 : 0.f;
-            bar.row_at[row] = live && ok ? at : -1;
-            tc_fence_before();
-            bar_sync(2, 256);
-        }
-        const int c0 = merge ? s * HALF : 0;
+        const int c0 = merge || NS == 1 ? s * HALF : 0;
         const bool other = merge && (s ? tiles > 0 : tiles > 1);
         if (ok)
-            put_rows<D, KV8>(a, smem + warp * S::STAGE, o_addr + c0, c0, S::BOTH || merge ? HALF : D, f0, any, f1, other ? from + row * PITCH : nullptr,
+            put_rows<D, KV8>(a, smem + warp * S::STAGE, o_addr + c0, c0, NS == 1 || merge ? HALF : D, f0, any, f1, other ? from + row * PITCH : nullptr,
                              final ? nullptr : part, r_here - lane, live ? at : -1, KV8 ? io_bf : BF);
-        tc_fence_before();
-    }
-    if (S::BOTH && warp >= W_TMA && warp < W_TMA + 4) {
-        // ---- the second half of a 256-wide output
-        bar_sync(2, 256);
-        tc_fence_after();
-        const int row = 32 * (warp % 4) + lane, at = bar.row_at[row];
-        const AttnUnit v = again(bar.unit[warp]);
-        float *part = a.part + (size_t)(v.slot + v.c) * a.M * (D + 2);
-        put_rows<D, KV8>(a, smem + warp * S::STAGE, tm + ((uint32_t)(32 * (warp % 4)) << 16) + S::COL_O + D / 2, D / 2, D / 2, bar.row_f[row],
-                         steps > 0, 0.f, nullptr, v.ranges == 1 ? nullptr : part, row - lane, at, KV8 ? io_bf : BF);
         tc_fence_before();
     }
     __syncthreads();
