@@ -564,7 +564,7 @@ AttnPlan attn_plan(int B, int total, int G, int D, bool kv8) {
     // each of 4 key heads: D = 128 in 16 bits 218 us on warps and 201 in tiles, in 8 bits 198 and 349, D = 64 128 and 163.
     // D = 256 holds 16 rows a warp.
     if (rows > (D == 256 || (D == 128 && !kv8) ? 16 : 32) && G <= 128)
-        return {true, 128 / G * G * (D == 256 ? 1 : 2), kAttnSms, kAttnSms, D == 256 ? 64 : 128, 512, 600, 200};
+        return {true, 128 / G * G * (D == 256 ? 1 : 2), kAttnSms, kAttnSms, D == 256 ? 64 : 128, 256, 600, 150};
     const int resident = D == 256 ? (kv8 ? 2 : 1) : 3;  // CTAs an SM
     return {false, rows <= 16 ? 16 : 32, resident * kAttnSms, 8 * kAttnSms, 64, 64, 400, 100};
 }

@@ -138,6 +138,7 @@ __device__ __forceinline__ bool attn_unit(const AttnArgs &a, int idx, AttnUnit &
     };
     const int least = a.min_range >> unit_log2;
     int most = max(at_least(few ? a.wave : a.target), least);
+    if (few && longest <= (most << unit_log2) + a.join_cost) most = 16777215;  // joining would take longer than the rest
     if (!few) {
         const int units = (longest + a.align - 1) >> unit_log2, mine = attn_ceil_div(max(units, 1), lane + 1);
         const float t = attn_time(a, tiles_all, all, (float)longest, (float)mine * (float)a.align);
