@@ -11,10 +11,10 @@
 // 16- or 32-token pieces of the range through a private ring in shared memory (cp.async, XOR-swizzled
 // chunks) and never waits for another warp until the end, where the warps' m, sums and outputs are
 // merged. Pages are multiples of 16 tokens, so 16 tokens are one contiguous segment of the pool.
-// Measured back to back on a GB300: 64 single tokens over up to 8,000 bf16 tokens each (8 x 4 heads of 128)
-// 179 us, 6.1 TB/s, 90 % of the copy rate; 64 blocks of 1 to 4 tokens over up to 25,000 in 8 bits 388 us, 5.0 TB/s: there
-// the conversions keep the integer pipe at 54 % with 2.6 warps a scheduler. One token over 1,000 takes 9.9 us,
-// which is latency: 1.7 us to find the unit, 1.2 to a page's first bytes, 2.5 for the join and 1.3 between the two.
+// Measured on a GB300: 64 single tokens over ragged caches of about 8,000 bf16 tokens (8 x 4 heads of 128) 179 us,
+// 6.1 TB/s, 90 % of the copy rate; 64 blocks of about 4 tokens over ragged 25,000 in 8 bits 388 us, 5.0 TB/s (counters of
+// 24 such requests: ALU pipe 54 %, issue slots 39 %, 2.6 warps a scheduler). One token over 1,000 (24 x 256 heads) takes
+// about 9.8 us on the device for 0.6 us of bytes: latency.
 //
 // 8-bit caches. The e4m3 values go to fp16 in registers, exactly; the rows' powers of two never
 // touch them. A key's exponent multiplies its score in 32 bits. A value's exponent multiplies its
@@ -556,9 +556,9 @@ attn_join_kernel(const __grid_constant__ AttnArgs a, bool bf) {
 
 // ---- host: which kernel, and how many units ---------------------------------------------------
 
-// Ranges are cut from 256 tokens on in tiles and from 64 on warps: 64 rows over 1,200 tokens of 8 x 128-wide heads
-// took 17.5, 14.5 and 13.3 us with ranges of at least 1,024, 512 and 256 tokens, one token over 1,000 of 4 x 256 13.0 and
-// 10.2 us with 256 and 64. unit_cost and join_cost are those that fitted 200 mixes of lengths best.
+// Tiles' ranges are of 256 tokens or more. 64 rows over 1,200 tokens of 8 x 128-wide heads took 17.5, 14.5 and 13.3 us
+// with at least 1,024, 512 and 256; over 600 tokens not to cut was better (11.2 us against 12.8), which join_cost
+// is for. Over 96 shapes of 600 to 5,000 tokens, 256 was 8 % faster than 512 and 1,024 9 % slower.
 struct AttnPlan {
     bool tc;
     int M, wave, target, align, min_range, unit_cost, join_cost;
@@ -645,8 +645,8 @@ extern "C" dn_status dn_attn_paged(int B, int total, int heads_kv, int group, in
         return DN_ERR_INVALID_ARG;
     AttnPlan p = attn_plan(B, total, group, D, cache_dt == DN_E4M3);
     if (pages == 0 || max_pages == 0) p = {false, 16, kAttnSms, kAttnSms, 64, 64, 400, 100};  // nothing is cached: no pool to copy from
-    // At most this many units: few tiles are cut for one wave (CTAs without a unit cost their launch, 5 us for
-    // 1,000 of the largest), and a table of few pages bounds the ranges of a tile.
+    // At most this many units: few tiles are cut for one wave (CTAs without a unit still cost their launch),
+    // and a table of few pages bounds the ranges of a tile.
     const long long whole = attn_tiles_bound(B, total, group, p.M) * heads_kv;
     if (2 * whole < p.wave) p.target = p.wave;
     const long long units = std::min(std::max(p.target, p.wave) + whole,

@@ -8,11 +8,11 @@
 // same columns if D = 128); P V is added to an accumulator. S(j + 2) may overwrite P(j) because products of
 // one shape run in the order of their issue; for the other D the shapes differ and P has its own columns.
 // The tensor core runs S(0), S(1), then P V(j), S(j + 2), .., so one step's softmax always has another
-// step's products beside it. For D <= 128 the even and the odd steps are two streams with a warpgroup and an accumulator each: if the unit has more
-// than 128 rows (a prompt's chunk) the streams are its two halves of rows over the same keys, else
-// (a verify block) they are the even and the odd key tiles of the same rows, merged at the end. For D = 256
-// an accumulator takes half of the tensor memory: one stream, key tiles of 64 tokens, of which each of the two
-// warpgroups has half of the columns.
+// step's products beside it. For D <= 128 the even and the odd steps are two streams with a warpgroup and an
+// accumulator each: if the unit has more than 128 rows (a prompt's chunk) the streams are its two halves of
+// rows over the same keys, else (a verify block) they are the even and the odd key tiles of the same rows,
+// merged at the end. For D = 256 an accumulator takes half of the tensor memory: one stream, key tiles of
+// 64 tokens, of which each of the two warpgroups has half of the columns.
 //
 // Copies. K and V tiles pass through one ring of shared-memory slots in the order in which the products take
 // them. Pages come in by TMA, one box per page and 64 columns, with the 128-byte swizzle that the MMA
@@ -32,13 +32,11 @@
 // probabilities are at most 2^8, rounded to 16 bits with the same relative step, and the division by the
 // sum at the end takes the factor out again.
 //
-// What bounds it, measured on a GB300. A prompt's chunk (2,048 tokens behind 22,952, 32 x 128 heads, bf16) takes
-// 565 us, 1,424 TFLOP/s, 74 % of the measured cuBLAS rate: its 256 units are 1.7 waves of 152, which costs 16 %, and
-// in a unit the tensor pipe is busy 64 to 88 % of the time, the softmax of two warps a scheduler the rest. A verify
-// block (96 rows of D = 256 over 25,000 tokens) takes 34 us against 15 for its bytes: 16 us at the copy rate, the rest
-// the unit's beginning (4 us) and end, and the join (5 us). 8-bit tiles cost their conversion, about 45 instructions
-// for 16 elements, and a ring of three 16-bit slots is what fits beside q: 268,000 tokens take 175 us against 81. For
-// D = 64 the exponentials, one for 256 operations, are the floor rather than the products.
+// Measured on a GB300. A prompt's chunk (2,048 tokens, 25,000 cached with them, 32 x 128 heads, bf16) takes about
+// 565 us, 1,425 TFLOP/s, 74 % of cuBLAS's rate: its 256 units are 1.7 waves of 152 (84 % of two). A verify block
+// (96 rows of D = 256 over 25,000 tokens, 16 bits) takes 34 us for 15 us of bytes: one wave, of which about 8 us
+// are its end and the join. Over 268,000 tokens in 8 bits it takes 175 us for 81: a 64-token tile takes 2,750 to 3,300
+// cycles by clock stamps, 1,400 would be the copy rate; three 16-bit slots are what fits beside q.
 //
 // Every wait is bounded in time; a wait that runs out raises the CTA's abort flag, and every role
 // leaves after its own copies and products have landed.
