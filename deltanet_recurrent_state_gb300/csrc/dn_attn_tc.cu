@@ -32,8 +32,9 @@
 // probabilities are at most 2^8, rounded to 16 bits with the same relative step, and the division by the
 // sum at the end takes the factor out again.
 //
-// Measured on a GB300. A prompt's chunk (2,048 tokens, 25,000 cached with them, 32 x 128 heads, bf16) takes about
-// 565 us, 1,425 TFLOP/s, 74 % of cuBLAS's rate: its 256 units are 1.7 waves of 152 (84 % of two). A verify block
+// Measured on a GB300. A prompt's chunk (2,048 tokens, 25,000 cached with them, 32 x 128 heads, bf16) takes 587 us,
+// 1,370 TFLOP/s, 71 % of cuBLAS's rate (about 565 back to back on one input): its 256 units are 1.7 waves of 152,
+// 84 % of two, and a chunk of 1,216 over 8,192 keeps the tensor pipe active 64 % of the cycles. A verify block
 // (96 rows of D = 256 over 25,000 tokens, 16 bits) takes 34 us for 15 us of bytes: one wave, of which about 8 us
 // are its end and the join. Over 268,000 tokens in 8 bits it takes 175 us for 81: a 64-token tile takes 2,750 to 3,300
 // cycles by clock stamps, 1,400 would be the copy rate; three 16-bit slots are what fits beside q.
