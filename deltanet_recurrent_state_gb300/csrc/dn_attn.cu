@@ -437,7 +437,7 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a, bool io_bf) {
         }
     __syncthreads();
     const bool final = u.ranges == 1;
-    float *part = a.part + (size_t)(u.slot + u.c) * M * (D + 2);
+    float *part = a.part + (u.slot + u.c) * attn_slot(M, D);
     for (int x = threadIdx.x; x < rows * (D / 4); x += 32 * W) {
         const int r = x / (D / 4), d = 4 * (x % (D / 4));
         float top = -INFINITY;
@@ -498,7 +498,7 @@ attn_join_kernel(const __grid_constant__ AttnArgs a, bool bf) {
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
     float top = -INFINITY, sum = 0.f;
     if (r < rows) {
-        const size_t slot = (size_t)M * (D + 2);
+        const size_t slot = attn_slot(M, D);
         const float *p = a.part + u.slot * slot;
         const int per = (u.ranges + WPR - 1) / WPR, c0 = w * per, c1 = min(u.ranges, c0 + per);
 #pragma unroll 4
@@ -619,7 +619,7 @@ extern "C" size_t dn_attn_workspace_bytes(int B, int total, int heads_kv, int gr
     size_t most = 0;
     for (int kv8 = 0; kv8 < 2; ++kv8) {
         const AttnPlan p = attn_plan(B, total, group, D, kv8);
-        most = std::max(most, (size_t)(2 * std::max(p.target, p.wave) + 64) * p.M * (D + 2) * sizeof(float));
+        most = std::max(most, (2 * std::max(p.target, p.wave) + 64) * attn_slot(p.M, D) * sizeof(float));
     }
     return most;
 }

@@ -36,7 +36,7 @@ struct AttnArgs {
     const uint8_t *ke, *ve;
     void *out;
     float *lse;   // may be null
-    float *part;  // slots of M * (D + 2) floats
+    float *part;  // slots of attn_slot(M, D) floats
     int G;
     float scale_log2;  // scale * log2(e): scores are kept in powers of two
     int window;        // 0: none
@@ -55,6 +55,10 @@ struct AttnUnit {
     int ranges;            // ranges of this tile that see anything (at least 1)
     int slot;              // workspace slot of range 0 of this tile (ranges > 1)
 };
+
+// Floats of a slot: M rows of D, then M pairs (maximum, sum). Rows are read and written four floats at a time, so
+// every slot begins on 16 bytes, also where a tile has an odd number of rows (D = 256 with 5 heads: 125).
+__host__ __device__ constexpr size_t attn_slot(int M, int D) { return ((size_t)M * (D + 2) + 3) / 4 * 4; }
 
 __host__ __device__ inline long long attn_tiles_bound(int B, int total, int G, int M) {
     const long long rows = (long long)total * G;

@@ -785,7 +785,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
         // the row's place in out and lse; a slot's rows are dense
         const bool live = row < mq_rows && r_here < v.n * a.G - first;
         const int token = (first + r_here) / a.G, at = (v.s + token) * (a.p.heads * a.G) + v.h * a.G + (first + r_here - token * a.G);
-        float *part = a.part + (size_t)(v.slot + v.c) * a.M * (D + 2);
+        float *part = a.part + (v.slot + v.c) * attn_slot(a.M, D);
         if (ok && live && !((merge || NS == 1) && s == 1)) {
             if (!final) *reinterpret_cast<float2 *>(part + (size_t)a.M * D + 2 * r_here) = make_float2(top, sum);
             else if (a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.693147180559945f;

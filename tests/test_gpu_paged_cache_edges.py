@@ -1,0 +1,34 @@
+"""The paged cache on the GPU where it can go wrong: groups, extreme sizes of values, windows, streams, lengths.
+
+The attention is held to the bounds that tests/test_gpu_paged_cache.py derives, unless a test states its own.
+Outputs are filled with NaN before every call, so that what a call leaves unwritten shows.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from deltanet_recurrent_state_gb300 import binding as dn
+from tests.test_gpu_paged_cache import E4M3, Setup, check_attn, n64
+
+pytestmark = pytest.mark.gpu
+
+
+def attend(s, window=0, scale=None, where=None):
+    out = torch.full(s.q.shape, float("nan"), dtype=s.io, device="cuda")
+    lse = torch.full(s.q.shape[:2], float("nan"), dtype=torch.float32, device="cuda")
+    dn.dn_attn_paged(s.q.cuda(), *(where or s.where()), window=window, scale=scale, out=out, lse=lse)
+    assert dn.dn_attn_wait_timeouts() == 0
+    return out, lse
+
+
+# ---- groups -------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("io,cache", [("f16", "io"), ("bf16", "io"), ("bf16", "e4m3")])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("group", [5, 11, 33, 128])
+def test_groups_of_many_heads_in_tiles(cuda, group, D, io, cache):
+    """D = 256 with 5, 11 or 33 heads a key head: tiles of an odd number of rows, cut into ranges and joined."""
+    s = Setup([16, 3], [2000, 700], 1, D, 64, io, cache, seed=group, group=group)
+    check_attn(s, *attend(s))
