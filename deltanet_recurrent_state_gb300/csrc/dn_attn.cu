@@ -569,11 +569,12 @@ AttnPlan attn_plan(int B, int total, int G, int D, bool kv8) {
     const long long rows = B > 0 ? ((long long)total * G + B - 1) / B : 0;
     // Warp MMAs up to 16 rows, and up to 32 where tcgen05 tiles are no faster: 64 requests x 8,000 tokens, 24 rows of
     // each of 4 key heads: D = 128 in 16 bits 218 us on warps and 201 in tiles, in 8 bits 198 and 349, D = 64 128 and 163.
-    // D = 256 holds 16 rows a warp.
-    if (rows > (D == 256 || (D == 128 && !kv8) ? 16 : 32) && G <= 128)
+    // D = 256 holds 16 rows a warp. A group of more than 128 heads has more rows than a tcgen05 tile: warp MMAs.
+    const int most = D == 256 || (D == 128 && !kv8) ? 16 : 32;
+    if (rows > most && G <= 128)
         return {true, 128 / G * G * (D == 256 ? 1 : 2), kAttnSms, kAttnSms, D == 256 ? 64 : 128, 256, 600, 150};
     const int resident = D == 256 ? (kv8 ? 2 : 1) : 3;  // CTAs an SM
-    return {false, rows <= 16 ? 16 : 32, resident * kAttnSms, 8 * kAttnSms, 64, 64, 400, 100};
+    return {false, rows <= 16 ? 16 : most, resident * kAttnSms, 8 * kAttnSms, 64, 64, 400, 100};
 }
 
 template <int D, int MT, bool BF, bool KV8>
@@ -584,12 +585,14 @@ void launch_rows(const AttnArgs &a, bool io_bf, unsigned grid, cudaStream_t st) 
 }
 
 template <int D, int MT>
-void launch_rows(const AttnArgs &a, bool bf, bool kv8, unsigned grid, cudaStream_t st) {
+bool launch_rows(const AttnArgs &a, bool bf, bool kv8, unsigned grid, cudaStream_t st) {
+    if (a.M != 16 * MT) return false;
     if (kv8) launch_rows<D, MT, false, true>(a, bf, grid, st);
     else if constexpr (D == 64 || MT == 1) {
         if (bf) launch_rows<D, MT, true, false>(a, bf, grid, st);
         else launch_rows<D, MT, false, false>(a, bf, grid, st);
-    }
+    } else return false;
+    return true;
 }
 
 }  // namespace
@@ -676,14 +679,16 @@ extern "C" dn_status dn_attn_paged(int B, int total, int heads_kv, int group, in
     a.soft = !p.tc;
     const bool bf = io_dt == DN_BF16, kv8 = cache_dt == DN_E4M3;
     cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
+    bool launched = true;
     if (p.tc && pages > 0 && max_pages > 0) {
         const dn_status ok = launch_attn_tc(a, D, bf, kv8, (unsigned)units, st);
         if (ok != DN_OK) return ok;
-    } else if (D == 64 && p.M == 16) launch_rows<64, 1>(a, bf, kv8, (unsigned)units, st);
-    else if (D == 64) launch_rows<64, 2>(a, bf, kv8, (unsigned)units, st);
-    else if (D == 128 && p.M == 16) launch_rows<128, 1>(a, bf, kv8, (unsigned)units, st);
-    else if (D == 128) launch_rows<128, 2>(a, bf, kv8, (unsigned)units, st);
-    else launch_rows<256, 1>(a, bf, kv8, (unsigned)units, st);
+    } else if (D == 64 && p.M == 16) launched = launch_rows<64, 1>(a, bf, kv8, (unsigned)units, st);
+    else if (D == 64) launched = launch_rows<64, 2>(a, bf, kv8, (unsigned)units, st);
+    else if (D == 128 && p.M == 16) launched = launch_rows<128, 1>(a, bf, kv8, (unsigned)units, st);
+    else if (D == 128) launched = launch_rows<128, 2>(a, bf, kv8, (unsigned)units, st);
+    else launched = launch_rows<256, 1>(a, bf, kv8, (unsigned)units, st);
+    if (!launched) return DN_ERR_UNSUPPORTED;  // (a plan for a kernel that is not there)
     if (units > whole) launch_attn_join(a, D, bf, st);  // (else no tile can have two ranges)
     return launch_status();
 }

@@ -32,3 +32,12 @@ def test_groups_of_many_heads_in_tiles(cuda, group, D, io, cache):
     """D = 256 with 5, 11 or 33 heads a key head: tiles of an odd number of rows, cut into ranges and joined."""
     s = Setup([16, 3], [2000, 700], 1, D, 64, io, cache, seed=group, group=group)
     check_attn(s, *attend(s))
+
+
+@pytest.mark.parametrize("cache", ["io", "e4m3"])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,kv,group", [([1], [900], 129), ([2, 0, 3], [40, 9, 700], 160)])
+def test_groups_of_more_heads_than_a_tile_has_rows(cuda, n, kv, group, D, cache):
+    s = Setup(n, kv, 1, D, 32, "f16", cache, seed=group, group=group)
+    check_attn(s, *attend(s))
+    check_attn(s, *attend(s, window=70), window=70)
