@@ -188,7 +188,7 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a, bool io_bf) {
                 // q = (q 2^-e) 2^e with the largest of the row in [1, 2)
                 const int e = min(max((int)(__float_as_uint(big) >> 23) - 127, -126), 126);
                 s2[hh] = __int_as_float((127 - e) << 23);
-                row_scale[mt][hh] = a.scale_log2 * __int_as_float((127 + e) << 23);
+                row_scale[mt][hh] = score_factor(a.scale_log2, e);
             }
             if (S::QREG || warp == 0) {
 #pragma unroll

@@ -575,7 +575,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
         const int tok = (row0 + r_unit) / a.G, pos = u.first + tok;
         // positions of the first and last row of the stream, for whole tiles without a mask
         const int tok_first = (row0 + (two_q ? s * mq_rows : 0)) / a.G, pos_first = u.first + tok_first, pos_last = pos_first + 128 / a.G - 1;
-        float q_factor = a.scale_log2;
+        int q_exp = 0;
         bool ok = true, any = false;
         if (KV8 && io_bf && tiles > 0) {
             // bf16 rows to fp16 by a power of two, in place (which chunk is which does not matter here)
@@ -618,7 +618,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             }
             mbar_arrive(&bar.q_ready);
             bar_sync(1, S::SOFTMAX);
-            q_factor *= __int_as_float((127 + bar.q_exp[two_q ? tid : row]) << 23);
+            q_exp = bar.q_exp[two_q ? tid : row];
         }
         const uint32_t lanes = (uint32_t)(32 * (warp % 4)) << 16;
         const uint32_t o_addr = tm + lanes + S::COL_O + (NS == 2 ? s * S::O_STEP : 0);
@@ -633,11 +633,11 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             uint32_t x[HELD][32];
 #pragma unroll
             for (int i = 0; i < HELD; ++i) tmem_ld32_start(s_addr + 32 * i, x[i]);
-            float factor = q_factor;
+            float factor = a.scale_log2;
             int ref_now = 0;
             if (KV8) {
                 if (!wait_for(&bar.ref_full[t & 3], (t >> 2) & 1, abort)) ok = false;
-                factor *= exp_byte(bar.k_ref[t & 3]);
+                factor = score_factor(a.scale_log2, q_exp + bar.k_ref[t & 3] - 127);
                 ref_now = bar.v_ref[t & 3];
             }
             tmem_wait_ld(x);

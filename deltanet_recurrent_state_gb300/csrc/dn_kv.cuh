@@ -41,6 +41,14 @@ __device__ __forceinline__ void packed_rows(const KvPool &p, int b, int &s, int 
 // 2^(E - 127) for a stored exponent byte (E = 0 is the subnormal 2^-127).
 __device__ __forceinline__ float exp_byte(int E) { return __int_as_float(E ? E << 23 : 0x00400000); }
 
+// scale * 2^e, the factor of a row's scores, kept away from 0 and infinity: masked scores are -inf before they are
+// multiplied, and -inf * 0 is NaN, as is the product of infinity and a score of 0.
+__device__ __forceinline__ float score_factor(float scale, int e) {
+    e = min(max(e, -252), 252);
+    const int h = e >> 1;  // in two steps, each a normal power
+    return fminf(fmaxf(scale * __int_as_float((127 + h) << 23) * __int_as_float((127 + e - h) << 23), 0x1p-149f), 3e38f);
+}
+
 // The exponent byte of a row whose largest magnitude is `big`: the fraction bits of 448 are 1.75,
 // so a larger fraction carries into the exponent. Zero, subnormal and tiny rows give 0.
 __device__ __forceinline__ int exponent_of(float big) {

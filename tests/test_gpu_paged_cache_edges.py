@@ -41,3 +41,19 @@ def test_groups_of_more_heads_than_a_tile_has_rows(cuda, n, kv, group, D, cache)
     s = Setup(n, kv, 1, D, 32, "f16", cache, seed=group, group=group)
     check_attn(s, *attend(s))
     check_attn(s, *attend(s, window=70), window=70)
+
+
+# ---- extreme sizes ------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("scale", [None, 2.0 ** -30])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rows", [2, 40, 300])
+def test_queries_and_keys_of_zero(cuda, rows, D, scale):
+    """Scores of 0 under a mask: the mean of the values that a row sees, and the log of their number."""
+    s = Setup([rows], [rows + 150], 1, D, 64, "bf16", "e4m3", seed=rows)
+    codes, E = s.d["k"]
+    held = s.own[:, None, :].expand(E.shape)
+    codes[held], E[held] = 0, 0
+    s.q[:] = 0
+    s.q[rows // 2, :, 0] = 2.0 ** -120
+    check_attn(s, *attend(s, scale=scale), scale=scale)
