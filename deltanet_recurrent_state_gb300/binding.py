@@ -94,6 +94,29 @@ def _stream(stream):
     return int(stream)
 
 
+def _other(stream):
+    """The torch stream of `stream` if it is not the current one, else None."""
+    if stream is None or _stream(stream) == _stream(None):
+        return None
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+
+
+def _new(other, make, kept=True):
+    """A tensor that a call makes for itself, from make(). The allocator hands memory out again in the order of the
+    stream it was made on, so that has to be the launch's stream; `kept` ones go to the caller, whose work on
+    the current stream the allocator then waits for too.
+    """
+    if other is None:
+        return make()
+    with torch.cuda.stream(other):
+        t = make()
+    if kept and t.is_cuda:
+        t.record_stream(torch.cuda.current_stream())
+    return t
+
+
 def _check(name, status):
     if status != DN_OK:
         raise DnError(name, status)
@@ -126,10 +149,11 @@ def dn_verify_block(q, k, v, beta, g, state_in, out=None, ckpt=None, stream=None
     """
     N, T, H, dk = q.shape
     dv = v.shape[-1]
+    other = _other(stream)
     if out is None:
-        out = torch.empty((N, T, H, dv), dtype=q.dtype, device=q.device)
+        out = _new(other, lambda: torch.empty((N, T, H, dv), dtype=q.dtype, device=q.device))
     if ckpt is None:
-        ckpt = torch.empty((N, T, H, dv, dk), dtype=state_in.dtype, device=q.device)
+        ckpt = _new(other, lambda: torch.empty((N, T, H, dv, dk), dtype=state_in.dtype, device=q.device))
     _dev(q, k, v, beta, g, state_in, out, ckpt)
     _require(k.shape == q.shape and v.shape == (N, T, H, dv), "k like q, v [N,T,H,dv]")
     _require(beta.shape == (N, T, H) and g.shape == (N, T, H), "beta, g [N,T,H]")
@@ -149,10 +173,11 @@ def dn_verify_block_deltas(q, k, v, beta, g, state_in, out=None, delta=None, str
     """As dn_verify_block, but writes delta [N,T,H,dv] fp32 instead of checkpoints."""
     N, T, H, dk = q.shape
     dv = v.shape[-1]
+    other = _other(stream)
     if out is None:
-        out = torch.empty((N, T, H, dv), dtype=q.dtype, device=q.device)
+        out = _new(other, lambda: torch.empty((N, T, H, dv), dtype=q.dtype, device=q.device))
     if delta is None:
-        delta = torch.empty((N, T, H, dv), dtype=torch.float32, device=q.device)
+        delta = _new(other, lambda: torch.empty((N, T, H, dv), dtype=torch.float32, device=q.device))
     _dev(q, k, v, beta, g, state_in, out, delta)
     _require(k.shape == q.shape and v.shape == (N, T, H, dv) and state_in.shape == (N, H, dv, dk),
              "k like q, v [N,T,H,dv], state_in [N,H,dv,dk]")
@@ -194,12 +219,13 @@ def dn_accept_greedy(logits, draft_ids, target_ids=None, accepted_len=None, work
     """logits [B,T,V] fp16/fp32, draft_ids [B,T] int32 -> (target_ids [B,T], accepted_len [B])."""
     B, T, V = logits.shape
     dev = logits.device
+    other = _other(stream)
     if target_ids is None:
-        target_ids = torch.empty((B, T), dtype=torch.int32, device=dev)
+        target_ids = _new(other, lambda: torch.empty((B, T), dtype=torch.int32, device=dev))
     if accepted_len is None:
-        accepted_len = torch.empty((B,), dtype=torch.int32, device=dev)
+        accepted_len = _new(other, lambda: torch.empty((B,), dtype=torch.int32, device=dev))
     if workspace is None:
-        workspace = accept_workspace(B, T, V, dev)
+        workspace = _new(other, lambda: accept_workspace(B, T, V, dev), kept=False)
     _dev(logits, draft_ids, target_ids, accepted_len, workspace)
     _require(draft_ids.shape == (B, T) and draft_ids.dtype == torch.int32, "draft_ids [B,T] int32")
     _require(target_ids.shape == (B, T) and accepted_len.shape == (B,), "target_ids [B,T], accepted_len [B]")
@@ -254,12 +280,13 @@ def dn_prefill_checkpoint(q, k, v, beta, g, state_in=None, out=None, ckpt=None, 
     dv = v.shape[-1]
     sdt = state_in.dtype if state_in is not None else (state_dtype or q.dtype)
     dev = q.device
+    other = _other(stream)
     if out is None:
-        out = torch.empty((N, P, H, dv), dtype=q.dtype, device=dev)
+        out = _new(other, lambda: torch.empty((N, P, H, dv), dtype=q.dtype, device=dev))
     if ckpt is None:
-        ckpt = torch.empty((N, P // chunk, H, dv, dk), dtype=sdt, device=dev)
+        ckpt = _new(other, lambda: torch.empty((N, P // chunk, H, dv, dk), dtype=sdt, device=dev))
     if state_out is None:
-        state_out = torch.empty((N, H, dv, dk), dtype=sdt, device=dev)
+        state_out = _new(other, lambda: torch.empty((N, H, dv, dk), dtype=sdt, device=dev))
     _dev(q, k, v, beta, g, state_in, out, ckpt, state_out)
     _require(k.shape == q.shape and v.shape == (N, P, H, dv) and beta.shape == (N, P, H),
              "k like q, v [N,P,H,dv], beta [N,P,H]")
@@ -296,12 +323,13 @@ def dn_context_drafts(context, lengths, n_max=4, n_min=1, K=8, drafts=None, coun
     """
     N, stride = context.shape
     dev = context.device
+    other = _other(stream)
     if drafts is None:
-        drafts = torch.empty((N, K), dtype=torch.int32, device=dev)
+        drafts = _new(other, lambda: torch.empty((N, K), dtype=torch.int32, device=dev))
     if count is None:
-        count = torch.empty((N,), dtype=torch.int32, device=dev)
+        count = _new(other, lambda: torch.empty((N,), dtype=torch.int32, device=dev))
     if match_len is None:
-        match_len = torch.empty((N,), dtype=torch.int32, device=dev)
+        match_len = _new(other, lambda: torch.empty((N,), dtype=torch.int32, device=dev))
     _dev(context, lengths, drafts, count, match_len)
     _require(context.dtype == lengths.dtype == drafts.dtype == count.dtype == torch.int32,
              "context, lengths, drafts, count int32")
@@ -426,12 +454,13 @@ def dn_attn_paged(q, start, kv_len, page_table, k_cache, v_cache, k_exp=None, v_
         raise ValueError("q's heads a multiple of the cache's")
     heads = shape[1]
     total, qs, dt = _rows(q, heads, D, "q")
+    other = _other(stream)
     if out is None:
-        out = torch.empty((total, heads, D), dtype=q.dtype, device=q.device)
+        out = _new(other, lambda: torch.empty((total, heads, D), dtype=q.dtype, device=q.device))
     if lse is None:
-        lse = torch.empty((total, heads), dtype=torch.float32, device=q.device)
+        lse = _new(other, lambda: torch.empty((total, heads), dtype=torch.float32, device=q.device))
     if workspace is None:
-        workspace = attn_workspace(q, k_cache, page_table)
+        workspace = _new(other, lambda: attn_workspace(q, k_cache, page_table), kept=False)
     if not (out.is_cuda and out.is_contiguous() and lse.is_cuda and lse.is_contiguous() and workspace.is_cuda
             and workspace.is_contiguous()):
         raise ValueError("out, lse and workspace are contiguous CUDA tensors")

@@ -57,3 +57,62 @@ def test_queries_and_keys_of_zero(cuda, rows, D, scale):
     s.q[:] = 0
     s.q[rows // 2, :, 0] = 2.0 ** -120
     check_attn(s, *attend(s, scale=scale), scale=scale)
+
+
+# ---- streams ------------------------------------------------------------------------------------
+
+def slow(ms):
+    torch.cuda._sleep(int(ms * 1.5e6))
+
+
+def test_workspace_of_a_call_on_another_stream(cuda):
+    """What the call allocated for itself is not handed out again while the call is still waiting to run."""
+    s = Setup([16], [3000], 2, 128, 64, "f16", "io", group=3)
+    w, q = s.where(), s.q.cuda()
+    want = [t.clone() for t in dn.dn_attn_paged(q, *w)]
+    bytes_ = dn.attn_workspace(q, w[3], w[2]).numel()
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            slow(50)
+        out, lse = dn.dn_attn_paged(q, *w, stream=stream)
+        mine = [torch.full((bytes_,), 7, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        torch.cuda.synchronize()
+        assert all((m == 7).all() for m in mine)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+        del mine
+
+
+def test_outputs_of_a_call_on_another_stream(cuda):
+    """Outputs do not take memory that work queued on the current stream still uses."""
+    s = Setup([16], [300], 2, 128, 64, "f16", "io", group=3)
+    w, q = s.where(), s.q.cuda()
+    ws = dn.attn_workspace(q, w[3], w[2])
+    dn.dn_attn_paged(q, *w, workspace=ws)
+    side = torch.cuda.Stream()
+    copy = torch.empty_like(q)
+    old = torch.full_like(q, 7.0)
+    torch.cuda.synchronize()
+    slow(50)
+    copy.copy_(old)
+    del old
+    out, _ = dn.dn_attn_paged(q, *w, workspace=ws, stream=side)
+    torch.cuda.synchronize()
+    assert (copy == 7).all()
+
+
+def test_accept_on_another_stream(cuda):
+    """The same of dn_accept_greedy, whose workspace has to be zero when the call runs."""
+    logits = torch.randn((2, 16, 4096), device="cuda").half()
+    drafts = torch.zeros((2, 16), dtype=torch.int32, device="cuda")
+    want = [t.clone() for t in dn.dn_accept_greedy(logits, drafts)]
+    n = dn.accept_workspace(2, 16, 4096, logits.device).numel()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        slow(50)
+    got = dn.dn_accept_greedy(logits, drafts, stream=side)
+    mine = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and all((m == 255).all() for m in mine)
