@@ -23,10 +23,11 @@
 // box, so a tile is as many whole tokens as 128 rows hold.
 //
 // 8-bit caches. The boxes land in a ring of raw tiles, and a warpgroup turns them into fp16 tiles, multiplied
-// by the powers of two 2^(E - R) <= 1 of the tokens: R is the tile's largest exponent for the keys, whose
-// 2^R joins the score's factor, and the largest so far for the values, so that tiles add up. Both products
-// are exact until an element falls below fp16's 2^-24, which is 2^-33 of the largest element. bf16 q is
-// brought to fp16 by a power of two for each row, as in dn_attn.cu.
+// by the powers of two 2^(E - R + 7) of the tokens: R is the tile's largest exponent for the keys, whose
+// 2^R joins the score's factor, and the largest so far for the values, so that tiles add up. The largest e4m3,
+// 448, becomes 57,344 at most, inside fp16's range; at the other end elements are rounded once, to multiples of 2^-24,
+// which is 2^-40 of that (without the 7 binades, 2^-33). The largest element may be one that a row does not
+// see. bf16 q is brought to fp16 by a power of two for each row, as in dn_attn.cu.
 //
 // Running maximum. O is rescaled only when a row's maximum grows by more than 2^8: until then its
 // probabilities are at most 2^8, rounded to 16 bits with the same relative step, and the division by the
@@ -143,6 +144,8 @@ __device__ __forceinline__ bool elect_one() {
     return r;
 }
 
+constexpr int TILE_UP = 7;  // binades that an 8-bit tile's elements are raised by: 448 * 2^7 = 57,344 is inside fp16's range
+
 template <int D, bool KV8>
 struct TileShape {
     static constexpr int NS = D <= 128 ? 2 : 1;      // streams
@@ -192,7 +195,7 @@ struct Bars {
     // by kind (keys, values) and tile modulo 4
     unsigned long long full[2][4], empty[2][4], raw_full[2][4], raw_empty[2][4], pow_full[2][4], ref_full[4], s_full[2], p_full[2], most_full[2], pv, q_full, q_ready, last_v, fin;
     uint32_t tmem;
-    int abort, k_ref[4], v_ref[4];
+    int abort, k_ref[4], v_ref[4], tiny[2][4];
     AttnUnit unit[8];  // the unit again, for the end (a copy a warp: held in registers it would cost the softmax some)
     signed char q_exp[256];  // powers of two of bf16 q rows brought to fp16
 };
@@ -494,13 +497,17 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             if (t >= 4 && (!wait_for(&bar.empty[1][t & 3], ((t - 4) >> 2) & 1, abort) ||
                            !wait_for(&bar.raw_empty[is_v][t & 3], ((t - 4) >> 2) & 1, abort)))
                 break;
+            bool tiny = false;
             if (4 * lane < BN) {
-                // 2^(E - R) in fp16, twice: subnormal below 2^-14, zero below 2^-24
+                // 2^(E - R + 7) in fp16, twice: subnormal below 2^-14. Below 2^-24 it comes as 2^-24 in the low half and the
+                // rest in the high one, with its sign set; from 2^-34 on even 448 times it rounds to 0
                 unsigned f[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const int E = (int)(((is_v ? ev : ek) >> (8 * e)) & 0xffu) - R;
-                    f[e] = (E >= -14 ? (unsigned)(15 + E) << 10 : E >= -24 ? 1u << (24 + E) : 0u) * 0x10001u;
+                    const int E = (int)(((is_v ? ev : ek) >> (8 * e)) & 0xffu) - R + TILE_UP;
+                    f[e] = E >= -24 ? (E >= -14 ? (unsigned)(15 + E) << 10 : 1u << (24 + E)) * 0x10001u
+                                    : E >= -33 ? 0x80000001u | (unsigned)(15 + 24 + E) << 26 : 0u;
+                    tiny |= (int)f[e] < 0;
                 }
                 *reinterpret_cast<uint4 *>(smem + S::OFF_POW + ((is_v * 4 + (t & 3)) * BN + 4 * lane) * 4) = make_uint4(f[0], f[1], f[2], f[3]);
             }
@@ -509,8 +516,12 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                 bar.v_ref[t & 3] = most;
                 mbar_arrive(&bar.ref_full[t & 3]);
             }
+            tiny = __any_sync(0xffffffffu, tiny);
             __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.pow_full[is_v][t & 3]);
+            if (lane == 0) {
+                bar.tiny[is_v][t & 3] = tiny;
+                mbar_arrive(&bar.pow_full[is_v][t & 3]);
+            }
         }
     } else if (KV8 && warp >= W_TMA + 4) {
         if (S::SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::R_OTHER));
@@ -561,6 +572,22 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                     const int first = half & 1;  // lanes of neighbouring halves store to different banks
                     *reinterpret_cast<uint4 *>(row + (((ch + first) ^ (r & 7)) << 4)) = first ? o[1] : o[0];
                     *reinterpret_cast<uint4 *>(row + (((ch + 1 - first) ^ (r & 7)) << 4)) = first ? o[0] : o[1];
+                }
+            }
+            if (bar.tiny[is_v][t & 3]) {
+                // rows whose power is below 2^-24, again: its high half first, exactly (e4m3 are multiples of 2^-9)
+#pragma unroll 1
+                for (int x = c; x < CHUNKS; x += KV8 ? S::CVT : 1) {
+                    const int r = x / (D / 16), e = x % (D / 16) * 16, half = e / 64, ch = e % 64 / 8;
+                    const unsigned f = mine[r], hi = (f >> 16 & 0x7fffu) * 0x10001u, lo = 0x10001u;
+                    if ((int)f >= 0 || r >= live) continue;
+#pragma unroll 1
+                    for (int i = 0; i < 8; ++i) {
+                        const unsigned h = unpack_e4m3(*reinterpret_cast<const unsigned short *>(src + x * 16 + 2 * i));
+                        const __half2 y = __hmul2(*reinterpret_cast<const __half2 *>(&h), *reinterpret_cast<const __half2 *>(&hi));
+                        *reinterpret_cast<__half2 *>(dst + half * BN * 128 + r * 128 + (((ch + i / 4) ^ (r & 7)) << 4) + i % 4 * 4) =
+                            __hmul2(y, *reinterpret_cast<const __half2 *>(&lo));
+                    }
                 }
             }
             fence_proxy_async();
@@ -627,21 +654,20 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
         for (int j = NS == 2 ? s : 0; ok && j < steps; j += NS) {
             const int t = two_q ? j >> 1 : j, j0 = u.lo + t * BN;
             const uint32_t s_addr = tm + lanes + (j & 1) * BN + (NS == 1 ? s * CN : 0), p_addr = tm + lanes + S::COL_P + (j & 1) * S::P_STEP + (NS == 1 ? s * CN / 2 : 0);
+            float factor = a.scale_log2;
+            int ref_now = 0;
+            if (KV8) {  // (known up to four tiles ahead of the scores)
+                if (!wait_for(&bar.ref_full[t & 3], (t >> 2) & 1, abort)) { ok = false; break; }
+                factor = score_factor(a.scale_log2, q_exp + bar.k_ref[t & 3] - 127 - TILE_UP);
+                ref_now = bar.v_ref[t & 3];
+            }
             if (!wait_for(&bar.s_full[j & 1], (j >> 1) & 1, abort)) { ok = false; break; }
             tc_fence_after();
             constexpr int HELD = S::TWICE ? 2 : CN / 32;  // groups of 32 columns held in registers
             uint32_t x[HELD][32];
 #pragma unroll
             for (int i = 0; i < HELD; ++i) tmem_ld32_start(s_addr + 32 * i, x[i]);
-            float factor = a.scale_log2;
-            int ref_now = 0;
-            if (KV8) {
-                if (!wait_for(&bar.ref_full[t & 3], (t >> 2) & 1, abort)) ok = false;
-                factor = score_factor(a.scale_log2, q_exp + bar.k_ref[t & 3] - 127);
-                ref_now = bar.v_ref[t & 3];
-            }
             tmem_wait_ld(x);
-            if (!ok) break;
             // columns least < i <= most are seen, as bits of each 32
             const bool edge = j0 + BN - 1 > pos_first || j0 + BN > u.hi || (a.window && j0 <= pos_last - a.window);
             const int c0 = NS == 1 ? s * CN : 0, most = min(pos, u.hi - 1) - j0 - c0, least = a.window ? pos - a.window - j0 - c0 : -1 - c0;
@@ -740,7 +766,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
         // ---- the outputs
         if (steps > 0 && ok) ok = wait_for(&bar.fin, 0, abort);
         tc_fence_after();
-        const float unit = KV8 ? ex2((float)(ref - 127)) : 1.f;
+        const float unit = KV8 ? ex2((float)(ref - 127 - TILE_UP)) : 1.f;
         const AttnUnit v = again(bar.unit[warp]);
         const int first = v.t * a.M, r_here = (NS == 2 && two_q ? s * mq_rows : 0) + row;
         const bool merge = NS == 2 && !two_q, final = v.ranges == 1;

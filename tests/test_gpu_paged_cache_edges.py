@@ -116,3 +116,40 @@ def test_accept_on_another_stream(cuda):
     mine = [torch.full((n,), 255, dtype=torch.uint8, device="cuda") for _ in range(2)]
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(got, want)) and all((m == 255).all() for m in mine)
+
+
+def put(s, x, c):
+    """Replaces the pool of x by the 8-bit form of c."""
+    codes, E = oracle.quantise(n64(c))
+    s.d[x] = (torch.from_numpy(codes), torch.from_numpy(E))
+
+
+@pytest.mark.parametrize("small", [4e-6, 4e-8])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rows,ctx", [(40, 88), (300, 84)])
+def test_small_rows_beside_a_large_one_that_is_not_seen(cuda, rows, ctx, D, small):
+    """8 bits: a draft of 448 that only the last row sees takes nothing from rows of 4 * 10^-6 or 4 * 10^-8 in its tile.
+
+    A tile's elements are on a grid of 2^-24 where its largest row ends at 448 * 2^7: with 448, off by at most
+    2^-32. For the values that is the error of the output; for the keys, times scale * sum |q|, that of a score
+    (relative, twice, that of a probability). q's elements below 2^-14 of the row's largest are off by 2^-25 of it.
+    """
+    s = Setup([rows], [rows + ctx], 1, D, 64, "bf16", "e4m3", seed=D, dirty=False)
+    g = torch.Generator().manual_seed(rows)
+    last = int(s.table[0, (rows + ctx - 1) // 64]), (rows + ctx - 1) % 64
+    for x in "kv":
+        c = (torch.randn(s.d[x][0].shape, generator=g) * small).bfloat16()
+        c[last[0], :, last[1]] = 448.0
+        put(s, x, c)
+    s.q = (torch.randn(s.q.shape, generator=g) * 0.25 / (small * D ** 0.5)).bfloat16()
+    out, lse = attend(s, scale=1.0)
+    q, k, v = n64(s.q), s.values("k"), s.values("v")
+    ref, rlse, weight, size = oracle.attn_paged(q, s.start.numpy(), s.kv, s.table.numpy(), k, v, 1.0)
+    ds = 2 * (2.0 ** -24 * (D + 4) * size + 2.0 ** -22 * (1 + size) + 2.0 ** -32 * np.abs(q).sum(-1)
+              + 2.0 ** -25 * np.abs(q).max(-1) * D * 5 * small)
+    tol = (2.0 ** -11 + ds[..., None] + 2.0 ** -20) * weight + 2.0 ** -32 + 2.0 ** -8 * np.abs(ref)
+    seen = slice(0, rows - 1)
+    d = np.abs(n64(out) - ref)[seen]
+    assert (d <= tol[seen]).all(), "out: %.3g of the bound" % (d / tol[seen]).max()
+    dl = np.abs(n64(lse) - rlse)[seen]
+    assert (dl <= ds[seen] + 2.0 ** -22 * (1 + np.abs(rlse[seen]))).all()
