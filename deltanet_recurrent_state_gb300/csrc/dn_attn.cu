@@ -422,7 +422,9 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a, bool io_bf) {
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
             if (t4 == 0) ml[warp * M + r] = make_float2(m[mt][hh], sum);
             float *dst = mo + (warp * M + r) * D;
-            const float f = KV8 ? exp2_fast((float)(ref - 127 - 15)) : 1.f;
+            // 2^(ref - 127 - 15) in two steps: the power itself may be below the smallest float, and the outputs are not
+            const float unit = exp_byte(ref);
+            auto out = [&](float x) { return x * 0x1p-15f * unit; };
             if (!KV8) {
 #pragma unroll
                 for (int j = 0; j < D / 8; ++j)
@@ -431,8 +433,8 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a, bool io_bf) {
 #pragma unroll
                 for (int c = 0; c < D / 16; ++c)  // columns 16 c + 4 t4 .. + 3: even, odd, even, odd
                     *reinterpret_cast<float4 *>(dst + 16 * c + 4 * t4) =
-                        make_float4(f * o[mt][2 * c][2 * hh], f * o[mt][2 * c + 1][2 * hh], f * o[mt][2 * c][2 * hh + 1],
-                                    f * o[mt][2 * c + 1][2 * hh + 1]);
+                        make_float4(out(o[mt][2 * c][2 * hh]), out(o[mt][2 * c + 1][2 * hh]), out(o[mt][2 * c][2 * hh + 1]),
+                                    out(o[mt][2 * c + 1][2 * hh + 1]));
             }
         }
     __syncthreads();

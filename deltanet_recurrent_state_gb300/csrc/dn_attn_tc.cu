@@ -224,14 +224,14 @@ __device__ __forceinline__ AttnUnit again(AttnUnit &from) {
     return u;
 }
 
-// One warp's 32 rows (lane: row) x `cols` columns of an accumulator, times f0, plus f1 times `other` (the row's
-// values in shared memory, or null), to out (part null) or to a slot of the workspace; `at` is the row of out,
+// One warp's 32 rows (lane: row) x `cols` columns of an accumulator, times f0 and (8 bits) then `unit`, whose product may
+// be below the smallest float where the outputs are not, plus f1 times `other` (the row's values in shared memory, or null), to out (part null) or to a slot of the workspace; `at` is the row of out,
 // -1 where there is none. EC columns at a time pass through shared memory, so that EC / 4 lanes write a row's
 // neighbouring columns: a lane writing its own row would touch 32 lines a store. Tensor-memory loads are the
 // whole warp's, whatever its rows.
 template <int D, bool KV8>
-__device__ __forceinline__ void put_rows(const AttnArgs &a, void *shared, uint32_t addr, int c0, int cols, float f0, bool any, float f1,
-                                         const float *other, float *part, int row0, int at, bool bf) {
+__device__ __forceinline__ void put_rows(const AttnArgs &a, void *shared, uint32_t addr, int c0, int cols, float f0, float unit, bool any,
+                                         float f1, const float *other, float *part, int row0, int at, bool bf) {
     constexpr int EC = KV8 || D == 64 ? 32 : 64, ER = 128 / EC;  // columns at a time, rows a store
     const int lane = threadIdx.x % 32;
     if (!__any_sync(0xffffffffu, at >= 0)) return;
@@ -250,6 +250,7 @@ __device__ __forceinline__ void put_rows(const AttnArgs &a, void *shared, uint32
             if (any)
                 z = make_float4(f0 * __uint_as_float(y[e / 32][e % 32]), f0 * __uint_as_float(y[e / 32][e % 32 + 1]),
                                 f0 * __uint_as_float(y[e / 32][e % 32 + 2]), f0 * __uint_as_float(y[e / 32][e % 32 + 3]));
+            if (KV8) z = make_float4(z.x * unit, z.y * unit, z.z * unit, z.w * unit);
             if (other) {
                 const float4 w = *reinterpret_cast<const float4 *>(other + d + e);
                 z = make_float4(fmaf(f1, w.x, z.x), fmaf(f1, w.y, z.y), fmaf(f1, w.z, z.z), fmaf(f1, w.w, z.w));
@@ -766,7 +767,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
         // ---- the outputs
         if (steps > 0 && ok) ok = wait_for(&bar.fin, 0, abort);
         tc_fence_after();
-        const float unit = KV8 ? ex2((float)(ref - 127 - TILE_UP)) : 1.f;
+        const float up = KV8 ? 1.f / (1 << TILE_UP) : 1.f, unit = KV8 ? exp_byte(ref) : 1.f;  // one after the other: see put_rows
         const AttnUnit v = again(bar.unit[warp]);
         const int first = v.t * a.M, r_here = (NS == 2 && two_q ? s * mq_rows : 0) + row;
         const bool merge = NS == 2 && !two_q, final = v.ranges == 1;
@@ -775,7 +776,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
         unsigned char *mine = smem + S::OFF_RING + 8192;  // (rows on their way out may take the bytes before)
         float *to = reinterpret_cast<float *>(mine) + s * 128 * PITCH, *from = reinterpret_cast<float *>(mine) + (1 - s) * 128 * PITCH;
         float2 *ml = reinterpret_cast<float2 *>(mine + 2 * 128 * PITCH * 4);
-        float top = m, f0 = unit, f1 = 0.f, sum = l;
+        float top = m, f0 = up, f1 = 0.f, sum = l;
         if (NS == 1) {  // the sum of the other half of the columns
             row_sum[s * 128 + row] = l;
             bar_sync(2, 256);
@@ -791,8 +792,8 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
 #pragma unroll
                 for (int e = 0; e < 32; e += 4)
                     *reinterpret_cast<float4 *>(to + row * PITCH + d + e) =
-                        make_float4(__uint_as_float(y[0][e]) * unit, __uint_as_float(y[0][e + 1]) * unit,
-                                    __uint_as_float(y[0][e + 2]) * unit, __uint_as_float(y[0][e + 3]) * unit);
+                        make_float4(__uint_as_float(y[0][e]) * up * unit, __uint_as_float(y[0][e + 1]) * up * unit,
+                                    __uint_as_float(y[0][e + 2]) * up * unit, __uint_as_float(y[0][e + 3]) * up * unit);
             }
             bar_sync(2, 256);
             const float2 y = ml[(1 - s) * 128 + row];
@@ -801,7 +802,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             f0 = ex2(m - base);
             f1 = ex2(y.x - base);
             sum = s ? f1 * y.y + f0 * l : f0 * l + f1 * y.y;
-            f0 *= unit;
+            f0 *= up;
         }
         if (final) {
             const float inv = sum > 0.f ? 1.f / sum : sum != sum ? sum : 0.f;  // NaN stays NaN
@@ -819,7 +820,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
         const int c0 = merge || NS == 1 ? s * HALF : 0;
         const bool other = merge && (s ? tiles > 0 : tiles > 1);
         if (ok)
-            put_rows<D, KV8>(a, smem + warp * S::STAGE, o_addr + c0, c0, NS == 1 || merge ? HALF : D, f0, any, f1, other ? from + row * PITCH : nullptr,
+            put_rows<D, KV8>(a, smem + warp * S::STAGE, o_addr + c0, c0, NS == 1 || merge ? HALF : D, f0, unit, any, f1, other ? from + row * PITCH : nullptr,
                              final ? nullptr : part, r_here - lane, live ? at : -1, KV8 ? io_bf : BF);
         tc_fence_before();
     }

@@ -153,3 +153,21 @@ def test_small_rows_beside_a_large_one_that_is_not_seen(cuda, rows, ctx, D, smal
     assert (d <= tol[seen]).all(), "out: %.3g of the bound" % (d / tol[seen]).max()
     dl = np.abs(n64(lse) - rlse)[seen]
     assert (dl <= ds[seen] + 2.0 ** -22 * (1 + np.abs(rlse[seen]))).all()
+
+
+@pytest.mark.parametrize("size", [-100, -112, -122])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rows", [1, 40, 300])
+def test_smallest_values_of_bf16(cuda, rows, D, size):
+    """Values of 2^-100 to 2^-122 in 8 bits come back with the precision of larger ones (bf16's grid ends at 2^-133)."""
+    s = Setup([rows], [rows + 700], 1, D, 64, "bf16", "e4m3", seed=D, dirty=False)
+    g = torch.Generator().manual_seed(rows)
+    put(s, "v", (torch.randn(s.d["v"][0].shape, generator=g, dtype=torch.float64) * 2.0 ** size).bfloat16())
+    out, lse = attend(s)
+    q, k, v = n64(s.q), s.values("k"), s.values("v")
+    ref, _, weight, x = oracle.attn_paged(q, s.start.numpy(), s.kv, s.table.numpy(), k, v, D ** -0.5)
+    ds = 2 * (2.0 ** -24 * (D + 4) * x + 2.0 ** -22 * (1 + x))
+    most = np.abs(v).max() * (rows + 700)
+    tol = (2.0 ** -11 + ds[..., None] + 2.0 ** -20) * weight + 2.0 ** -25 * most + 2.0 ** -8 * np.abs(ref) + 2.0 ** -133
+    d = np.abs(n64(out) - ref)
+    assert (d <= tol).all(), "out: %.3g of the bound" % (d / tol).max()
