@@ -77,6 +77,7 @@ struct RowsShape {
     // Ring stages. Two leave three CTAs an SM (96 KB in flight, and 12 warps to compute): with four, one CTA of
     // 4 warps, the batch of 64 single tokens (D = 128, 16-bit) took 266 us instead of 193.
     static constexpr int ST = D * EB >= 256 && !(D == 128) ? 3 : 2;
+    static constexpr int CTAS = MT == 2 ? 2 : D == 64 ? 4 : D == 128 ? 3 : KV8 ? 2 : 1;  // an SM: bounds the registers
     static constexpr int M = 16 * MT;
     static constexpr bool QREG = D * MT <= 128;               // q fragments in registers, else shared
     static constexpr size_t RING = (size_t)W * ST * STAGE;
@@ -86,7 +87,7 @@ struct RowsShape {
 };
 
 template <int D, int MT, bool BF, bool KV8>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(128, RowsShape<D, MT, KV8>::CTAS)
 attn_rows_kernel(const __grid_constant__ AttnArgs a, bool io_bf) {
     using S = RowsShape<D, MT, KV8>;
     constexpr int W = S::W, ST = S::ST, KS = D / 16, CPR = D * S::EB / 16, M = S::M, H = S::H, P = S::P;
@@ -104,7 +105,9 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a, bool io_bf) {
     unsigned char *ring = smem + (size_t)warp * ST * S::STAGE;
     const int pieces = max(0, ((u.hi - u.lo + P - 1) / P - warp + W - 1) / W);
     int page_ahead = -1;  // lane l: the pool page of this warp's 16 tokens number 32 * batch + l
-    auto load = [&](int i) {
+    // Tokens before the window are in the warps' first pieces alone: the range begins less than 64 tokens before it.
+    static_assert(P * W >= 64, "ranges begin at multiples of 64");
+    auto load = [&](int i, auto first) {
         if (i < pieces) {
             if (((i * H) & 31) == 0) page_ahead = pool_page(a.p, u.b, u.lo + P * (warp + W * (i + lane / H)) + 16 * (lane % H));
             unsigned char *st = ring + (i % ST) * S::STAGE;
@@ -113,17 +116,18 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a, bool io_bf) {
                 const int pg = __shfl_sync(0xffffffffu, page_ahead, (i * H + h) & 31);
                 const int j0 = u.lo + P * (warp + W * i) + 16 * h;
                 const long long row0 = ((((long long)max(pg, 0) * a.p.heads + u.h)) << a.p.page_shift) + (j0 & ((1 << a.p.page_shift) - 1));
-                const int live = pg < 0 ? 0 : min(16, u.hi - j0);  // rows past the range are zeros
+                const int live = pg < 0 ? 0 : min(16, u.hi - j0);  // rows past the range are zeros,
+                const int dead = first ? u.see - j0 : 0;           // as are those before the window
                 const unsigned char *ks = static_cast<const unsigned char *>(a.kc) + row0 * (D * S::EB) + lane * 16;
                 const unsigned char *vs = static_cast<const unsigned char *>(a.vc) + row0 * (D * S::EB) + lane * 16;
 #pragma unroll
                 for (int x = 0; x < 16 * CPR / 32; ++x) {
                     const int e = x * 32 + lane, at = h * S::HALF + 16 * chunk_at<CPR>(e / CPR, e % CPR);
-                    if (live >= 16) {
+                    if (live >= 16 && dead <= 0) {
                         cp_async16(st + at, ks + x * 512, 16);
                         cp_async16(st + S::TILE + at, vs + x * 512, 16);
                     } else {  // (nothing is read where the count is 0)
-                        const int bytes = e / CPR < live ? 16 : 0;
+                        const int bytes = e / CPR < live && e / CPR >= dead ? 16 : 0;
                         cp_async16(st + at, bytes ? ks + x * 512 : static_cast<const unsigned char *>(a.q), bytes);
                         cp_async16(st + S::TILE + at, bytes ? vs + x * 512 : static_cast<const unsigned char *>(a.q), bytes);
                     }
@@ -135,7 +139,10 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a, bool io_bf) {
         cp_async_commit();
     };
 #pragma unroll
-    for (int i = 0; i < ST - 1; ++i) load(i);
+    for (int i = 0; i < ST - 1; ++i) {
+        if (i == 0) load(i, std::true_type{});
+        else load(i, std::false_type{});
+    }
 
     // ---- q fragments: rows g and g + 8 of each 16-row tile
     unsigned qf[S::QREG ? MT : 1][S::QREG ? KS : 1][4];
@@ -229,7 +236,7 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a, bool io_bf) {
     for (int i = 0; i < pieces; ++i) {
         cp_async_wait<ST - 2>();
         __syncwarp();
-        load(i + ST - 1);
+        load(i + ST - 1, std::false_type{});
         const unsigned char *st = ring + (i % ST) * S::STAGE;
         const int j0 = u.lo + P * (warp + W * i);
         // ---- scores
@@ -282,17 +289,21 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a, bool io_bf) {
         // ---- exponents of the keys and values (tokens 8 nt + 2 t4, + 1 of this thread)
         float vf[2 * H][2];
         if (KV8) {
+            // bytes past the range or before the window are not of the rows'
+            const int see = a.window && i == 0 ? row0_pos - a.window + 1 : 0;
+            const bool part = j0 + P > u.hi || j0 < see;
             const unsigned char *ex = st + 2 * S::TILE;  // of each half: 16 keys', 16 values'
             unsigned top = 0;
 #pragma unroll
             for (int h = 0; h < H; ++h) {
                 const uint4 all = *reinterpret_cast<const uint4 *>(ex + 32 * h + 16);
                 unsigned w[4] = {all.x, all.y, all.z, all.w};
-                if (j0 + 16 * h + 16 > u.hi) {  // bytes past the range are not the request's
+                if (part) {
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
-                        const int livebytes = min(max(u.hi - j0 - 16 * h - 4 * x, 0), 4);
+                        const int livebytes = min(max(u.hi - j0 - 16 * h - 4 * x, 0), 4), deadbytes = min(max(see - j0 - 16 * h - 4 * x, 0), 4);
                         if (livebytes < 4) w[x] &= (1u << (8 * livebytes)) - 1u;
+                        w[x] = deadbytes < 4 ? w[x] & (0xffffffffu << (8 * deadbytes)) : 0u;
                     }
                 }
                 top = __vmaxu4(top, __vmaxu4(__vmaxu4(w[0], w[1]), __vmaxu4(w[2], w[3])));
@@ -318,12 +329,18 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a, bool io_bf) {
                     const float kf = exp_byte((k2 >> (8 * e)) & 0xffu);
                     const int x = (int)((v2 >> (8 * e)) & 0xffu) - ref + 15 + 127;
                     vf[nt][e] = __int_as_float(max(x, 0) << 23);
-                    if (j0 + 8 * nt + 2 * t4 + e >= u.hi) vf[nt][e] = 0.f;
 #pragma unroll
                     for (int mt = 0; mt < MT; ++mt) {
                         s[mt][nt][e] *= kf;
                         s[mt][nt][2 + e] *= kf;
                     }
+                }
+            }
+            if (part) {
+#pragma unroll
+                for (int x = 0; x < 4 * H; ++x) {
+                    const int j = j0 + 8 * (x / 2) + 2 * t4 + x % 2;
+                    if (j >= u.hi || j < see) vf[x / 2][x % 2] = 0.f;
                 }
             }
         }

@@ -51,7 +51,8 @@ struct AttnArgs {
 struct AttnUnit {
     int b, h, t, c;        // request, key head, tile, range
     int s, n, first, len;  // packed rows [s, s + n); position of the first; cached tokens
-    int lo, hi;            // cached tokens of this unit
+    int lo, hi;            // cached tokens of this unit; lo is rounded down to a multiple of align
+    int see;               // the first that any row of the tile sees: what a window leaves in lo .. see - 1 may hold anything
     int ranges;            // ranges of this tile that see anything (at least 1)
     int slot;              // workspace slot of range 0 of this tile (ranges > 1)
 };
@@ -202,8 +203,8 @@ __device__ __forceinline__ bool attn_unit(const AttnArgs &a, int idx, AttnUnit &
             u.slot = slots_before + from(slots_upto - slots) + (u.h * T + u.t) * R;
             const int r0 = u.t * a.M, r1 = min(a.M, u.n * a.G - r0) - 1 + r0;
             const int hi = min(max(u.first + attn_div(r1, a.G) + 1, 0), u.len);
-            int lo = a.window ? max(u.first + attn_div(r0, a.G) - a.window + 1, 0) : 0;
-            lo = min(lo & ~(a.align - 1), hi);
+            u.see = a.window ? max(u.first + attn_div(r0, a.G) - a.window + 1, 0) : 0;
+            const int lo = min(u.see & ~(a.align - 1), hi);
             u.ranges = hi - lo > step ? attn_ceil_div(hi - lo, step) : 1;
             u.lo = u.c < u.ranges ? lo + u.c * step : hi;
             u.hi = hi - u.lo > step ? u.lo + step : hi;

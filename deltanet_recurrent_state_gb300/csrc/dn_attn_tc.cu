@@ -18,8 +18,8 @@
 // them. Pages come in by TMA, one box per page and 64 columns, with the 128-byte swizzle that the MMA
 // descriptors read; the producer's lanes look the pages up 32 at a time. A page that a
 // request does not have is an out-of-range coordinate, which the copy fills with zeros. Rows of the last
-// page past the range may hold anything: their scores are masked, and their values are zeroed in
-// shared memory before the product (0 x NaN is not 0). q comes the same way, G heads by 128 / G tokens a
+// page past the range, and of the first one before a window, may hold anything: their scores are masked, and
+// their values are zeroed in shared memory before the product (0 x NaN is not 0). q comes the same way, G heads by 128 / G tokens a
 // box, so a tile is as many whole tokens as 128 rows hold.
 //
 // 8-bit caches. The boxes land in a ring of raw tiles, and a warpgroup turns them into fp16 tiles, multiplied
@@ -193,7 +193,7 @@ struct TileShape {
 
 struct Bars {
     // by kind (keys, values) and tile modulo 4
-    unsigned long long full[2][4], empty[2][4], raw_full[2][4], raw_empty[2][4], pow_full[2][4], ref_full[4], s_full[2], p_full[2], most_full[2], pv, q_full, q_ready, last_v, fin;
+    unsigned long long full[2][4], empty[2][4], raw_full[2][4], raw_empty[2][4], pow_full[2][4], ref_full[4], s_full[2], p_full[2], most_full[2], pv, q_full, q_ready, first_v, last_v, fin;
     uint32_t tmem;
     int abort, k_ref[4], v_ref[4], tiny[2][4];
     AttnUnit unit[8];  // the unit again, for the end (a copy a warp: held in registers it would cost the softmax some)
@@ -308,6 +308,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
         mbar_init(&bar.pv, 1);
         mbar_init(&bar.q_full, 1);
         mbar_init(&bar.q_ready, S::SOFTMAX);
+        mbar_init(&bar.first_v, 1);
         mbar_init(&bar.last_v, 1);
         mbar_init(&bar.fin, 1);
         bar.abort = 0;
@@ -335,6 +336,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
     const bool two_q = NS == 2 && rows > mq_rows;
     const int tiles = (u.hi - u.lo + BN - 1) / BN;
     const int steps = two_q ? 2 * tiles : tiles;
+    const int head = max(u.see - u.lo, 0);  // tokens of the first tile that no row sees (fewer than a tile)
     // the ring; without a second q tile, its place is one more slot
     const bool wide = NS == 2 && !two_q;
     unsigned char *ring = smem + S::OFF_RING - (wide ? S::QTILE : 0);
@@ -377,7 +379,8 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             }
             const int ids = x & 1 ? pages_odd : pages_even;
             const int slot = KV8 ? seq % (KV8 ? S::RAWS : 1) : slot_of(seq), j0 = u.lo + t * BN;
-            unsigned long long *full = KV8 ? &bar.raw_full[is_v][t & 3] : is_v && t == tiles - 1 ? &bar.last_v : &bar.full[is_v][t & 3];
+            unsigned long long *full = KV8 ? &bar.raw_full[is_v][t & 3] : is_v && t == tiles - 1 ? &bar.last_v
+                                       : is_v && t == 0 && head > 0 ? &bar.first_v : &bar.full[is_v][t & 3];
             if (seq >= NB) {  // what was in the slot before
                 int t0;
                 bool v0;
@@ -406,6 +409,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                 seq_tile(two_q, seq, tiles, t, is_v);
                 if (!KV8 && is_v != values) continue;
                 if (!KV8 && is_v && t == tiles - 1) mbar_drain(&bar.last_v, 0);
+                else if (!KV8 && is_v && t == 0 && head > 0) mbar_drain(&bar.first_v, 0);
                 else if (seq >= issued - NB) mbar_drain(KV8 ? &bar.raw_full[is_v][t & 3] : &bar.full[is_v][t & 3], (t >> 2) & 1);
             }
         }
@@ -458,16 +462,28 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
     } else if (!KV8 && warp >= W_TMA) {
         if (S::SPLIT) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::R_OTHER));
         if (warp == W_TMA + 2 && tiles > 0) {
-            // ---- the last tile's values past the range; its copy lands on a barrier of its own
-            const int slot = slot_of(seq_v(two_q, tiles - 1, tiles)), live = u.hi - (u.lo + (tiles - 1) * BN);
-            if (wait_for(&bar.last_v, 0, abort)) {
-                for (int i = lane; i < (BN - live) * 8 * S::HALVES; i += 32) {
-                    const int r = live + i / (8 * S::HALVES), c = i % (8 * S::HALVES);
+            // ---- the first tile's values before a window and the last one's past the range, whose copies land on
+            // barriers of their own
+            auto clear = [&](int t, int r0, int r1) {  // rows r0 .. r1 - 1 of value tile t
+                const int slot = slot_of(seq_v(two_q, t, tiles));
+                for (int i = lane; i < (r1 - r0) * 8 * S::HALVES; i += 32) {
+                    const int r = r0 + i / (8 * S::HALVES), c = i % (8 * S::HALVES);
                     *reinterpret_cast<uint4 *>(ring + slot * TILE + (c / 8) * BN * 128 + r * 128 + (c % 8) * 16) = make_uint4(0, 0, 0, 0);
                 }
+            };
+            auto hand_on = [&](int t) {
                 fence_proxy_async();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.full[1][(tiles - 1) & 3]);
+                if (lane == 0) mbar_arrive(&bar.full[1][t & 3]);
+            };
+            if (head > 0 && tiles > 1 && wait_for(&bar.first_v, 0, abort)) {
+                clear(0, 0, head);
+                hand_on(0);
+            }
+            if (wait_for(&bar.last_v, 0, abort)) {
+                if (tiles == 1) clear(0, 0, min(head, BN));
+                clear(tiles - 1, u.hi - (u.lo + (tiles - 1) * BN), BN);
+                hand_on(tiles - 1);
             }
         }
     } else if (KV8 && warp >= W_TMA && warp < W_TMA + 4) {
@@ -476,14 +492,15 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
         const bool is_v = warp == W_TMA + 3;
         int most = 0;  // the values' largest exponent so far
         for (int t = 0; t < tiles; ++t) {
-            // exponents of tokens 4 lane .. + 3; bytes past the range are not the request's
-            const int j = u.lo + t * BN + 4 * lane, live = u.hi - j;
+            // exponents of tokens 4 lane .. + 3; bytes past the range or before the window are not of the rows'
+            const int j = u.lo + t * BN + 4 * lane, live = u.hi - j, dead = u.see - j;
             unsigned ek = 0, ev = 0;
             if (4 * lane < BN && live > 0) {
                 const int pg = pool_page(a.p, u.b, j);
                 if (pg >= 0) {
                     const long long at = ((((long long)pg * a.p.heads + u.h)) << a.p.page_shift) + (j & ((1 << a.p.page_shift) - 1));
-                    const unsigned mask = live >= 4 ? 0xffffffffu : (1u << (8 * live)) - 1u;
+                    const unsigned mask = (live >= 4 ? 0xffffffffu : (1u << (8 * live)) - 1u) &
+                                          (dead <= 0 ? 0xffffffffu : dead >= 4 ? 0u : 0xffffffffu << (8 * dead));
                     ev = __ldg(reinterpret_cast<const unsigned *>(a.ve + at)) & mask;
                     if (!is_v) ek = __ldg(reinterpret_cast<const unsigned *>(a.ke + at)) & mask;
                 }
@@ -530,7 +547,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
         const bool is_v = tid - (W_TMA + 4) * 32 >= S::CVT;
         const int c = tid - (W_TMA + 4) * 32 - (is_v ? S::CVT : 0);
         for (int t = 0; t < tiles; ++t) {
-            const int seq = is_v ? seq_v(two_q, t, tiles) : seq_k(two_q, t), live = min(BN, u.hi - (u.lo + t * BN));
+            const int seq = is_v ? seq_v(two_q, t, tiles) : seq_k(two_q, t), live = min(BN, u.hi - (u.lo + t * BN)), dead = t == 0 ? head : 0;
             const int slot = slot_of(seq), rs = seq % (KV8 ? S::RAWS : 1);
             if (seq >= slots) {
                 int t0;
@@ -554,7 +571,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                     w[i] = make_uint4(0, 0, 0, 0);
                     if (i0 + i < PER && x < CHUNKS) {  // (a warp's 32 chunks at once)
                         f[i] = mine[r];
-                        if (r < live) w[i] = *reinterpret_cast<const uint4 *>(src + x * 16);  // rows past the range are zeros
+                        if (r < live && r >= dead) w[i] = *reinterpret_cast<const uint4 *>(src + x * 16);  // rows past the range or before the window are zeros
                     }
                 }
 #pragma unroll
@@ -581,7 +598,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                 for (int x = c; x < CHUNKS; x += KV8 ? S::CVT : 1) {
                     const int r = x / (D / 16), e = x % (D / 16) * 16, half = e / 64, ch = e % 64 / 8;
                     const unsigned f = mine[r], hi = (f >> 16 & 0x7fffu) * 0x10001u, lo = 0x10001u;
-                    if ((int)f >= 0 || r >= live) continue;
+                    if ((int)f >= 0 || r >= live || r < dead) continue;
 #pragma unroll 1
                     for (int i = 0; i < 8; ++i) {
                         const unsigned h = unpack_e4m3(*reinterpret_cast<const unsigned short *>(src + x * 16 + 2 * i));

@@ -171,3 +171,23 @@ def test_smallest_values_of_bf16(cuda, rows, D, size):
     tol = (2.0 ** -11 + ds[..., None] + 2.0 ** -20) * weight + 2.0 ** -25 * most + 2.0 ** -8 * np.abs(ref) + 2.0 ** -133
     d = np.abs(n64(out) - ref)
     assert (d <= tol).all(), "out: %.3g of the bound" % (d / tol).max()
+
+
+# ---- windows and lengths ------------------------------------------------------------------------
+
+@pytest.mark.parametrize("io,cache", [("f16", "io"), ("bf16", "io"), ("bf16", "e4m3")])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("n,kv,group,window", [([1], [1000], 1, 100), ([16, 3], [900, 150], 6, 77), ([150, 40], [410, 700], 2, 100),
+                                              ([300], [1200], 1, 513)])
+def test_what_lies_before_the_window_may_be_anything(cuda, n, kv, group, window, D, io, cache):
+    s = Setup(n, kv, 2, D, 64, io, cache, seed=window, group=group)
+    for b in range(len(n)):
+        for j in range(max(0, kv[b] - n[b] - window + 1)):
+            at = int(s.table[b, j // 64]), j % 64
+            s.own[at] = False
+            for x in "kv":
+                c, E = s.d[x]
+                c[at[0], :, at[1]] = float("nan") if E is None else 0x7F
+                if E is not None:
+                    E[at[0], :, at[1]] = 255
+    check_attn(s, *attend(s, window=window), window=window)
