@@ -84,7 +84,7 @@ struct AttnRequest {
 __device__ __forceinline__ AttnRequest attn_request(const AttnArgs &a, int b) {
     AttnRequest r;
     packed_rows(a.p, b, r.s, r.n);
-    const int held = min(max(__ldg(&a.p.kv_len[b]), 0), 1 << 30);
+    const int held = held_tokens(a.p, b);
     r.first = held - r.n;
     r.len = min(held, a.p.max_pages << a.p.page_shift);
     r.tiles = attn_ceil_div(r.n * a.G, a.M);  // (the host bounds total * heads by 2^31 - 1 - 1024)

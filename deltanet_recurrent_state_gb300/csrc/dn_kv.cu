@@ -43,7 +43,7 @@ __device__ __forceinline__ long long place_of(const KvPool &p, int t, int lane) 
     int s, n;
     packed_rows(p, b, s, n);
     if (t < s || t >= s + n) return -1;
-    const int pos = __ldg(&p.kv_len[b]) - n + (t - s);
+    const int pos = held_tokens(p, b) - n + (t - s);
     const int g = pool_page(p, b, pos);
     if (g < 0) return -1;
     return (((long long)g * p.heads) << p.page_shift) + (pos & ((1 << p.page_shift) - 1));

@@ -14,6 +14,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "dn.h"
+
 namespace dn {
 
 // Where a request's cached tokens are.
@@ -31,6 +33,9 @@ __device__ __forceinline__ int pool_page(const KvPool &p, int b, int pos) {
     const int g = __ldg(&p.table[(long long)b * p.max_pages + i]);
     return (unsigned)g < (unsigned)p.pages ? g : -1;
 }
+
+// Cached tokens of request b, 0 .. DN_KV_MAX_TOKENS whatever the value of kv_len.
+__device__ __forceinline__ int held_tokens(const KvPool &p, int b) { return min(max(__ldg(&p.kv_len[b]), 0), DN_KV_MAX_TOKENS); }
 
 // The packed rows [s, s + n) of request b, inside 0 .. total whatever the values of start.
 __device__ __forceinline__ void packed_rows(const KvPool &p, int b, int &s, int &n) {

@@ -191,3 +191,26 @@ def test_what_lies_before_the_window_may_be_anything(cuda, n, kv, group, window,
                 if E is not None:
                     E[at[0], :, at[1]] = 255
     check_attn(s, *attend(s, window=window), window=window)
+
+
+@pytest.mark.parametrize("cache", ["io", "e4m3"])
+def test_append_and_gather_clamp_the_length(cuda, cache):
+    """kv_len above the most tokens counts as that, as for the attention."""
+    s = Setup([2], [128], 1, 64, 128, "f16", cache, dirty=False)
+    w = s.where()
+    table = torch.full((1, 1 << 23), -1, dtype=torch.int32, device="cuda")  # 2^30 positions
+    table[0, -1] = s.table[0, 0]
+    k, v = (x.cuda() for x in s.new)
+    a, b = [t if t is None else t.clone() for t in w], [t if t is None else t.clone() for t in w]
+    a[2] = b[2] = table
+    a[1] = torch.tensor([1 << 30], dtype=torch.int32, device="cuda")
+    b[1] = torch.tensor([(1 << 30) + 1], dtype=torch.int32, device="cuda")
+    dn.dn_kv_append(k, v, *a)
+    dn.dn_kv_append(k, v, *b)
+    dn.dn_kv_append(k, v, *w)  # the same rows of the page, by a short table
+    for i in (3, 4):
+        assert torch.equal(a[i].view(torch.uint8), b[i].view(torch.uint8)) and torch.equal(a[i].view(torch.uint8), w[i].view(torch.uint8))
+    got, want = [[torch.full_like(x, float("nan")) for x in (k, v)] for _ in range(2)]
+    dn.dn_kv_gather(*b, *got)
+    dn.dn_kv_gather(*w, *want)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
