@@ -661,7 +661,7 @@ extern "C" dn_status dn_attn_paged(int B, int total, int heads_kv, int group, in
         !kv_pages_ok(max_pages, pages, page) || q_stride < (int64_t)heads_kv * group * D || q_stride % 8)
         return DN_ERR_INVALID_ARG;
     if (B == 0 || total == 0) return DN_OK;
-    if (!kv_pointers_ok(start, kv_len, page_table, k_cache, v_cache, k_exp, v_exp, cache_dt, pages, max_pages) || !q ||
+    if (!kv_pointers_ok(B, start, kv_len, page_table, k_cache, v_cache, k_exp, v_exp, cache_dt, pages, max_pages) || !q ||
         !out || !workspace || !aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 16) ||
         workspace_bytes < dn_attn_workspace_bytes(B, total, heads_kv, group, D))
         return DN_ERR_INVALID_ARG;

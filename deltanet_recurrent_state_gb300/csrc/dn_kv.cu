@@ -216,7 +216,7 @@ extern "C" dn_status dn_kv_append(int B, int total, int heads, int D, int page, 
         k_stride % 8 || v_stride % 8)
         return DN_ERR_INVALID_ARG;
     if (B == 0 || total == 0) return DN_OK;
-    if (!kv_pointers_ok(start, kv_len, page_table, k_cache, v_cache, k_exp, v_exp, cache_dt, pages, max_pages) ||
+    if (!kv_pointers_ok(B, start, kv_len, page_table, k_cache, v_cache, k_exp, v_exp, cache_dt, pages, max_pages) ||
         !k || !v || !aligned(k, 16) || !aligned(v, 16))
         return DN_ERR_INVALID_ARG;
     if (pages == 0 || max_pages == 0) return DN_OK;  // no place for any token
@@ -239,8 +239,7 @@ extern "C" dn_status dn_kv_gather(int B, int total, int heads, int D, int page, 
     if (ok != DN_OK) return ok;
     if (!kv_pages_ok(max_pages, pages, page)) return DN_ERR_INVALID_ARG;
     if (total == 0) return DN_OK;
-    if (!kv_pointers_ok(start, kv_len, page_table, k_cache, v_cache, k_exp, v_exp, cache_dt, pages,
-                        B == 0 ? 0 : max_pages) || !k || !v || !aligned(k, 16) || !aligned(v, 16))
+    if (!kv_pointers_ok(B, start, kv_len, page_table, k_cache, v_cache, k_exp, v_exp, cache_dt, pages, max_pages) || !k || !v || !aligned(k, 16) || !aligned(v, 16))
         return DN_ERR_INVALID_ARG;
     KvPool p = {start, kv_len, page_table, B, total, max_pages, pages, page_log2(page), heads};
     const int pieces = (heads * (D / 8) + 32 * kPasses - 1) / (32 * kPasses);

@@ -214,3 +214,13 @@ def test_append_and_gather_clamp_the_length(cuda, cache):
     dn.dn_kv_gather(*b, *got)
     dn.dn_kv_gather(*w, *want)
     assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def test_gather_of_no_request_gives_zeros(cuda):
+    s = Setup([2], [5], 1, 64, 16, "f16", "io", dirty=False)
+    w = s.where()
+    w[0], w[1] = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.empty(0, dtype=torch.int32, device="cuda")
+    w[2] = torch.empty((0, 1), dtype=torch.int32, device="cuda")
+    k, v = (torch.full((3, 1, 64), 9.0, dtype=torch.float16, device="cuda") for _ in range(2))
+    dn.dn_kv_gather(*w, k, v)
+    assert (k == 0).all() and (v == 0).all()

@@ -13,3 +13,11 @@ def test_workspace_slots_begin_on_16_bytes(lib):  # noqa: F811
     for D in (64, 128, 256):
         for group in range(1, 129):
             assert lib.dn_attn_workspace_bytes(1, 64, 1, group, D) % (16 * (2 * 152 + 64)) == 0, (D, group)
+
+
+def test_gather_without_requests_needs_no_lengths(lib):  # noqa: F811
+    """(Past the checks there is no device here, or a launch.)"""
+    import torch
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are no device memory")
+    assert lib.dn_kv_gather(*args("gather", B=0, kv=None, table=None)) != INVALID
