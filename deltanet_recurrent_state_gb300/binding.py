@@ -450,7 +450,7 @@ def dn_attn_paged(q, start, kv_len, page_table, k_cache, v_cache, k_exp=None, v_
     """
     B, heads_kv, D, page, max_pages, pages, cdt = _kv_pool(start, kv_len, page_table, k_cache, v_cache, k_exp, v_exp)
     shape = q.shape
-    if len(shape) != 3 or shape[1] % heads_kv or shape[1] < 1:
+    if len(shape) != 3 or heads_kv < 1 or shape[1] % heads_kv or shape[1] < 1:
         raise ValueError("q's heads a multiple of the cache's")
     heads = shape[1]
     total, qs, dt = _rows(q, heads, D, "q")

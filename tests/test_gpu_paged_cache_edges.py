@@ -224,3 +224,13 @@ def test_gather_of_no_request_gives_zeros(cuda):
     k, v = (torch.full((3, 1, 64), 9.0, dtype=torch.float16, device="cuda") for _ in range(2))
     dn.dn_kv_gather(*w, k, v)
     assert (k == 0).all() and (v == 0).all()
+
+
+# ---- the binding --------------------------------------------------------------------------------
+
+def test_a_cache_without_heads_is_refused(cuda):
+    s = Setup([2], [5], 1, 64, 16, "f16", "io", dirty=False)
+    w = s.where()
+    w[3], w[4] = w[3][:, :0].contiguous(), w[4][:, :0].contiguous()
+    with pytest.raises(ValueError):
+        dn.dn_attn_paged(s.q.cuda(), *w)
