@@ -445,7 +445,7 @@ def dn_attn_paged(q, start, kv_len, page_table, k_cache, v_cache, k_exp=None, v_
     """Attention of the newest tokens q [total,heads,D] over their requests' cached keys and values.
 
     The cache's tensors as for dn_kv_append; heads is a multiple of the cache's. scale defaults to
-    D ** -0.5; window is how many tokens a row looks back, itself included (0: all). q may be a slice of
+    D ** -0.5; window is how many tokens a row looks back, itself included (0, or 2^30 and more: all). q may be a slice of
     a wider projection. Returns (out [total,heads,D] in q's dtype, lse [total,heads] fp32).
     """
     B, heads_kv, D, page, max_pages, pages, cdt = _kv_pool(start, kv_len, page_table, k_cache, v_cache, k_exp, v_exp)
@@ -471,7 +471,7 @@ def dn_attn_paged(q, start, kv_len, page_table, k_cache, v_cache, k_exp=None, v_
     st = (_lib or load_library()).dn_attn_paged(
         B, total, heads_kv, heads // heads_kv, D, page, max_pages, pages, dt, cdt, q.data_ptr(), qs, start.data_ptr(),
         kv_len.data_ptr(), page_table.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_exp), _ptr(v_exp),
-        D ** -0.5 if scale is None else scale, window, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+        D ** -0.5 if scale is None else scale, max(-1, min(window, 1 << 30)), out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
         workspace.nbytes, _stream(stream))
     if st:
         _check("dn_attn_paged", st)

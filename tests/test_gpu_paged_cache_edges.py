@@ -234,3 +234,15 @@ def test_a_cache_without_heads_is_refused(cuda):
     w[3], w[4] = w[3][:, :0].contiguous(), w[4][:, :0].contiguous()
     with pytest.raises(ValueError):
         dn.dn_attn_paged(s.q.cuda(), *w)
+
+
+def test_windows_past_32_bits(cuda):
+    s = Setup([3], [200], 1, 64, 16, "f16", "io", dirty=False)
+    w, q = s.where(), s.q.cuda()
+    want = dn.dn_attn_paged(q, *w)
+    for window in ((1 << 32) + 5, 1 << 31, 1 << 64):
+        got = dn.dn_attn_paged(q, *w, window=window)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for window in (-1, -(1 << 32) + 5):
+        with pytest.raises(dn.DnError):
+            dn.dn_attn_paged(q, *w, window=window)
