@@ -16,6 +16,9 @@
 // 24 such requests: ALU pipe 54 %, issue slots 39 %, 2.6 warps a scheduler). One token over 1,000 (24 x 256 heads) takes
 // about 9.8 us on the device for 0.6 us of bytes: latency.
 //
+// fp16 probabilities are held as 2^15 p, which fp16 has room for (p <= 1): those below 2^-39 are lost to the product with the
+// values, not those below 2^-24, which many tokens of a long cache may have while the sum counts them.
+//
 // 8-bit caches. The e4m3 values go to fp16 in registers, exactly; the rows' powers of two never
 // touch them. A key's exponent multiplies its score in 32 bits. A value's exponent multiplies its
 // probability: p 2^(E - R + 15) <= 2^15 with R the largest exponent so far, rounded to fp16 for the
@@ -92,6 +95,7 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a, bool io_bf) {
     using S = RowsShape<D, MT, KV8>;
     constexpr int W = S::W, ST = S::ST, KS = D / 16, CPR = D * S::EB / 16, M = S::M, H = S::H, P = S::P;
     constexpr bool MB = BF && !KV8;  // type of the MMAs
+    constexpr float P_UP = MB || KV8 ? 0.f : 15.f, P_DOWN = MB || KV8 ? 1.f : 0x1p-15f;  // binades of the probabilities (KV8: in vf)
     extern __shared__ __align__(16) unsigned char smem[];
     const int lane = threadIdx.x % 32, warp = threadIdx.x / 32, g = lane >> 2, t4 = lane & 3;
     grid_dep_wait();
@@ -383,7 +387,7 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a, bool io_bf) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         float &x = s[mt][nt][2 * hh + e];
-                        x = exp2_fast(fmaf(x, row_scale[mt][hh], -base));
+                        x = exp2_fast(fmaf(x, row_scale[mt][hh], P_UP - base));
                         l[mt][hh] += x;
                         if (KV8) x *= vf[nt][e];
                     }
@@ -434,7 +438,7 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a, bool io_bf) {
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
             const int r = 16 * mt + g + 8 * hh;
-            float sum = l[mt][hh];
+            float sum = l[mt][hh] * P_DOWN;
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
             if (t4 == 0) ml[warp * M + r] = make_float2(m[mt][hh], sum);
@@ -445,7 +449,7 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a, bool io_bf) {
             if (!KV8) {
 #pragma unroll
                 for (int j = 0; j < D / 8; ++j)
-                    *reinterpret_cast<float2 *>(dst + 8 * j + 2 * t4) = make_float2(o[mt][j][2 * hh], o[mt][j][2 * hh + 1]);
+                    *reinterpret_cast<float2 *>(dst + 8 * j + 2 * t4) = make_float2(o[mt][j][2 * hh] * P_DOWN, o[mt][j][2 * hh + 1] * P_DOWN);
             } else {
 #pragma unroll
                 for (int c = 0; c < D / 16; ++c)  // columns 16 c + 4 t4 .. + 3: even, odd, even, odd

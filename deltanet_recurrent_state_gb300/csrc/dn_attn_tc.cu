@@ -31,7 +31,8 @@
 //
 // Running maximum. O is rescaled only when a row's maximum grows by more than 2^8: until then its
 // probabilities are at most 2^8, rounded to 16 bits with the same relative step, and the division by the
-// sum at the end takes the factor out again.
+// sum at the end takes the factor out again. fp16 ones are held as 2^7 p, up to 2^15: fp16's smallest number is then
+// 2^-31 (see dn_attn.cu).
 //
 // Measured on a GB300. A prompt's chunk (2,048 tokens, 25,000 cached with them, 32 x 128 heads, bf16) takes 587 us,
 // 1,370 TFLOP/s, 71 % of cuBLAS's rate (about 565 back to back on one input): its 256 units are 1.7 waves of 152,
@@ -144,6 +145,7 @@ __device__ __forceinline__ bool elect_one() {
     return r;
 }
 
+constexpr int P_UP = 7;     // binades that fp16 probabilities, at most 2^8, are raised by
 constexpr int TILE_UP = 7;  // binades that an 8-bit tile's elements are raised by: 448 * 2^7 = 57,344 is inside fp16's range
 
 template <int D, bool KV8>
@@ -751,7 +753,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                 }
             }
             const float base = m == -INFINITY ? 0.f : m;
-            const float2 f2 = make_float2(factor, factor), b2 = make_float2(-base, -base);
+            const float2 f2 = make_float2(factor, factor), b2 = make_float2((MB ? 0.f : (float)P_UP) - base, (MB ? 0.f : (float)P_UP) - base);
             float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             if (HELD < CN / 32) {
                 uint32_t(&y)[1][32] = reinterpret_cast<uint32_t(&)[1][32]>(x[0]);
@@ -784,7 +786,9 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
         // ---- the outputs
         if (steps > 0 && ok) ok = wait_for(&bar.fin, 0, abort);
         tc_fence_after();
-        const float up = KV8 ? 1.f / (1 << TILE_UP) : 1.f, unit = KV8 ? exp_byte(ref) : 1.f;  // one after the other: see put_rows
+        constexpr float p_down = MB ? 1.f : 1.f / (1 << P_UP);
+        const float up = KV8 ? p_down / (1 << TILE_UP) : p_down, unit = KV8 ? exp_byte(ref) : 1.f;  // one after the other: see put_rows
+        l *= p_down;
         const AttnUnit v = again(bar.unit[warp]);
         const int first = v.t * a.M, r_here = (NS == 2 && two_q ? s * mq_rows : 0) + row;
         const bool merge = NS == 2 && !two_q, final = v.ranges == 1;

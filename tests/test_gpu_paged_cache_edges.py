@@ -246,3 +246,31 @@ def test_windows_past_32_bits(cuda):
     for window in (-1, -(1 << 32) + 5):
         with pytest.raises(dn.DnError):
             dn.dn_attn_paged(q, *w, window=window)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rows", [1, 40, 300])
+def test_many_improbable_tokens_in_fp16(cuda, rows, D):
+    """Tokens whose probabilities are below fp16's smallest number each, and count together.
+
+    Every 2,000th key scores 17.5 above the others (by a product of 1 and 17.5, exact), with a value of 0 against 64:
+    out = 64 r / (1 + r) with r = 1,999 e^-17.5. Bounds: 2^-11 for a probability (2^-7 of it on the finest grid), 2^-11
+    for the output and its grid of 2^-24, and 2^-18 for the exponential and the sums.
+    """
+    heads, page, kv = 160, 128, 16000
+    pages = kv // page
+    k = torch.zeros((pages, heads, page, D), dtype=torch.float16, device="cuda")
+    v = torch.full_like(k, 64.0)
+    hot = torch.arange(0, kv, 2000, device="cuda") + 1000
+    k[hot // page, :, hot % page, 0], v[hot // page, :, hot % page] = 17.5, 0.0
+    q = torch.zeros((rows, heads, D), dtype=torch.float16, device="cuda")
+    q[:, :, 0] = 1.0
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    one = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    out, _ = dn.dn_attn_paged(q, one(0, rows), one(kv), table, k, v, scale=1.0)
+    # rows see kv - rows + 1 + i tokens: all hot ones (the last at 15,000), fewer others
+    others = torch.arange(kv - rows + 1, kv + 1, dtype=torch.float64) - 8
+    r = others / 8 * torch.exp(torch.tensor(-17.5, dtype=torch.float64))
+    ref = (64 * r / (1 + r))[:, None, None]
+    d = (out.double().cpu() - ref).abs()
+    assert (d <= (2.0 ** -7 + 2.0 ** -11 + 2.0 ** -18) * ref + 2.0 ** -25).all()
