@@ -600,6 +600,12 @@ AttnPlan attn_plan(int B, int total, int G, int D, bool kv8) {
     return {false, rows <= 16 ? 16 : most, resident * kAttnSms, 8 * kAttnSms, 64, 64, 400, 100};
 }
 
+// Sizes that the attention takes, as far as they are products.
+bool attn_sizes_ok(int total, int heads_kv, int group) {
+    const long long heads = (long long)heads_kv * group;
+    return heads <= (1 << 20) && total * heads <= 0x7fffffffLL - 1024;
+}
+
 template <int D, int MT, bool BF, bool KV8>
 void launch_rows(const AttnArgs &a, bool io_bf, unsigned grid, cudaStream_t st) {
     using S = RowsShape<D, MT, KV8>;
@@ -641,7 +647,9 @@ void launch_attn_join(const AttnArgs &a, int D, bool bf, cudaStream_t st) {
 
 extern "C" size_t dn_attn_workspace_bytes(int B, int total, int heads_kv, int group, int D) {
     using namespace dn;
-    if (B < 1 || total < 1 || total > DN_KV_MAX_ROWS || heads_kv < 1 || group < 1 || !kv_shape_ok(D, 16)) return 0;
+    if (B < 1 || total < 1 || total > DN_KV_MAX_ROWS || heads_kv < 1 || group < 1 || !kv_shape_ok(D, 16) ||
+        !attn_sizes_ok(total, heads_kv, group))
+        return 0;
     size_t most = 0;
     for (int kv8 = 0; kv8 < 2; ++kv8) {
         const AttnPlan p = attn_plan(B, total, group, D, kv8);
@@ -661,8 +669,7 @@ extern "C" dn_status dn_attn_paged(int B, int total, int heads_kv, int group, in
         !(scale > 0.f) || !(scale < 2e38f) || !kv_dtypes_known(io_dt, cache_dt))
         return DN_ERR_INVALID_ARG;
     if (!kv_shape_ok(D, page) || !kv_dtypes_ok(io_dt, cache_dt)) return DN_ERR_UNSUPPORTED;
-    if ((long long)heads_kv * group > (1 << 20) || (long long)total * heads_kv * group > 0x7fffffffLL - 1024 ||
-        !kv_pages_ok(max_pages, pages, page) || q_stride < (int64_t)heads_kv * group * D || q_stride % 8)
+    if (!attn_sizes_ok(total, heads_kv, group) || !kv_pages_ok(max_pages, pages, page) || q_stride < (int64_t)heads_kv * group * D || q_stride % 8)
         return DN_ERR_INVALID_ARG;
     if (B == 0 || total == 0) return DN_OK;
     if (!kv_pointers_ok(B, start, kv_len, page_table, k_cache, v_cache, k_exp, v_exp, cache_dt, pages, max_pages) || !q ||

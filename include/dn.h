@@ -430,6 +430,7 @@ dn_status dn_wait_selftest(int budget_us, int32_t *result, dn_stream_t stream);
  *   D         64, 128 or 256;  page 16, 32, 64 or 128 (64 is the prefix index's interval)
  *   io_dt     DN_F16 or DN_BF16;  cache_dt io_dt, or DN_E4M3 for 8 bits
  *   total     packed rows, 0 .. DN_KV_MAX_ROWS;  max_pages * page <= DN_KV_MAX_TOKENS
+ *   heads * D <= 2^24 (append, gather)
  * Another D, page or type pair gives DN_ERR_UNSUPPORTED. Rows of one request write to pages of its
  * own; two packed rows that name the same place leave one of them there.
  *
@@ -468,7 +469,8 @@ dn_status dn_kv_gather(int B, int total, int heads, int D, int page, int max_pag
  * single new token, a verify block and a chunk of a prompt, also mixed in one batch. A row that
  * sees nothing gets out = 0 and lse = -inf.
  *
- *   heads_kv, group  key heads, and query heads of each (heads_kv * group query heads)
+ *   heads_kv, group  key heads, and query heads of each (heads_kv * group query heads, at most 2^20;
+ *             total * heads_kv * group < 2^31 - 1024)
  *   q         row t at q + t * q_stride elements, [heads_kv * group][D] dense inside; io_dt, 16-byte
  *             aligned, q_stride a multiple of 8 and >= heads_kv * group * D
  *   scale     > 0 and < 2e38;  window  tokens that a row looks back, itself included; 0: all

@@ -21,3 +21,10 @@ def test_gather_without_requests_needs_no_lengths(lib):  # noqa: F811
     if torch.cuda.is_available():
         pytest.skip("the addresses are no device memory")
     assert lib.dn_kv_gather(*args("gather", B=0, kv=None, table=None)) != INVALID
+
+
+def test_no_workspace_for_sizes_that_are_refused(lib):  # noqa: F811
+    for B, total, heads, group in ((1, 4, 1 << 20, 2), (1, 1 << 28, 8, 1), (1, 1 << 28, 1, 8), (1, 1 << 27, 4, 4)):
+        assert lib.dn_attn_paged(*args("attn", B=B, total=total, heads=heads, group=group, qs=heads * group * 64)) == INVALID
+        assert lib.dn_attn_workspace_bytes(B, total, heads, group, 64) == 0
+    assert lib.dn_attn_workspace_bytes(1, 1 << 28, 1, 4, 64) > 0
