@@ -274,3 +274,23 @@ def test_many_improbable_tokens_in_fp16(cuda, rows, D):
     ref = (64 * r / (1 + r))[:, None, None]
     d = (out.double().cpu() - ref).abs()
     assert (d <= (2.0 ** -7 + 2.0 ** -11 + 2.0 ** -18) * ref + 2.0 ** -25).all()
+
+
+# ---- repeats ------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("io,cache", [("f16", "io"), ("bf16", "e4m3")])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("rows,group", [(1, 4), (40, 4), (300, 4), (16, 5), (1, 129)])
+def test_every_output_is_written_alike_again(cuda, rows, group, D, io, cache):
+    """Ranges that are joined, into outputs of NaN, with a workspace of ones (NaN too) and of zeros."""
+    s = Setup([rows, 5, 1], [3000, 900, 2500], 2, D, 64, io, cache, group=group)
+    w, q = s.where(), s.q.cuda()
+    got = []
+    for fill in (255, 0):
+        ws = dn.attn_workspace(q, w[3], w[2]).fill_(fill)
+        out = torch.full_like(q, float("nan"))
+        lse = torch.full(q.shape[:2], float("nan"), dtype=torch.float32, device="cuda")
+        got.append(dn.dn_attn_paged(q, *w, out=out, lse=lse, workspace=ws))
+    assert dn.dn_attn_wait_timeouts() == 0
+    assert all(torch.isfinite(t).all() for t in got[0])
+    assert all(torch.equal(a, b) for a, b in zip(*got))
