@@ -499,7 +499,7 @@ attn_rows_kernel(const __grid_constant__ AttnArgs a, bool io_bf) {
 }
 
 // ---- join: the ranges of a tile, in their order ----------------------------------------------
-// A CTA joins kJoinRows rows of one tile and head, its eight warps in equal groups a row: each warp adds
+// A CTA joins ROWS rows of one tile and head, its eight warps in equal groups a row: each warp adds
 // an eighth (or fewer) of the ranges, a lane holding D / 32 columns, and the warps' sums are added in order.
 // The partials were written by the launch before and are in L2; a row is few loads deep.
 template <int D, int ROWS>

@@ -425,7 +425,8 @@ dn_status dn_wait_selftest(int budget_us, int32_t *result, dn_stream_t stream);
  *
  * start, kv_len and page_table are read on the device (no host round trip after an accept). Nothing
  * in them leads outside the buffers: a position without a page (below 0, beyond max_pages * page, or
- * with a page id outside 0 .. pages-1) is not written, and reads as zeros.
+ * with a page id outside 0 .. pages-1) is not written, and reads as zeros. (The attention leaves out positions
+ * beyond max_pages * page: no row sees them.)
  *
  *   D         64, 128 or 256;  page 16, 32, 64 or 128 (64 is the prefix index's interval)
  *   io_dt     DN_F16 or DN_BF16;  cache_dt io_dt, or DN_E4M3 for 8 bits
@@ -462,7 +463,7 @@ dn_status dn_kv_gather(int B, int total, int heads, int D, int page, int max_pag
  *
  * For every packed row t of request b, at position p = kv_len[b] - n_b + (t - start[b]), and every
  * query head h = heads of the key head h / group:
- *   sees j  if  0 <= j <= p, j < kv_len[b], and (window > 0) j > p - window
+ *   sees j  if  0 <= j <= p, j < kv_len[b], j < max_pages * page, and (window > 0) j > p - window
  *   x_j = scale * q[t][h] . K_j[h / group];   lse[t][h] = log sum_j exp(x_j)
  *   out[t][h] = sum_j exp(x_j - lse) V_j[h / group]
  * The newest tokens' own keys and values are in the cache (append them first), so one call serves a
@@ -473,16 +474,20 @@ dn_status dn_kv_gather(int B, int total, int heads, int D, int page, int max_pag
  *             total * heads_kv * group < 2^31 - 1024)
  *   q         row t at q + t * q_stride elements, [heads_kv * group][D] dense inside; io_dt, 16-byte
  *             aligned, q_stride a multiple of 8 and >= heads_kv * group * D
- *   scale     > 0 and < 2e38;  window  tokens that a row looks back, itself included; 0: all
+ *   scale     > 0 and < 2e38;  window  tokens that a row looks back, itself included; 0, or 2^30 and more: all
  *   out       [total][heads_kv * group][D] io_dt, dense, 16-byte aligned, written
  *   lse       [total][heads_kv * group] fp32, written, or NULL
  *   workspace >= dn_attn_workspace_bytes(...) bytes, 16-byte aligned, any contents; calls that may
  *             run concurrently need separate ones
  * Packed rows of no request are left unwritten. Keys and values that a row of the call sees, or that
  * lie between those, are finite: probabilities of 0 still meet them in a product. What lies past
- * kv_len[b], or in pages that a request does not name, may be anything. Scores, maxima, sums and
- * outputs are kept in 32 bits; probabilities are rounded to 16 bits for the product with the
- * values. The order of all sums is fixed by the sizes and lengths: results repeat bit for bit.
+ * kv_len[b], before every row's window, or in pages that a request does not name, may be anything.
+ * Scores, maxima, sums and outputs are kept in 32 bits; probabilities are rounded to 16 bits (io_dt's form,
+ * fp16 for an 8-bit cache) for the product with the values, and vanish from it below 2^-31 of the largest.
+ * With an 8-bit cache, keys (calls of many rows) and values of a tile are brought to a common exponent in 16
+ * bits: what is below 2^-29 of the largest among them, seen by the row or not, may lose bits, and what is below
+ * 2^-39 vanishes; elements of a bf16 q below 2^-14 of its row's largest lose bits. The order of all sums is
+ * fixed by the sizes and lengths: results repeat bit for bit.
  *
  * dn_attn_workspace_bytes is 0 for sizes that dn_attn_paged refuses, B = 0 or total = 0.
  */
