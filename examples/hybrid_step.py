@@ -86,7 +86,8 @@ class HybridModel:
 
     def prompt(self, tokens):
         """Run all but the last token of a prompt; the last one begins the first verify block."""
-        self.forward(tokens[:-1], commit_all=True)
+        if tokens.numel() > 1:
+            self.forward(tokens[:-1], commit_all=True)
         self.last = tokens[-1:]
 
     def verify(self, drafts):
@@ -112,6 +113,8 @@ def main():
     ap.add_argument("--steps", type=int, default=4)
     ap.add_argument("--cache", choices=["f16", "e4m3"], default="f16")
     args = ap.parse_args()
+    if args.prompt < 1:
+        ap.error("a prompt has a token at least")
     model = HybridModel(cache=args.cache, max_tokens=args.prompt + T * (args.steps + 1))
     g = torch.Generator(device="cuda")
     g.manual_seed(1)
