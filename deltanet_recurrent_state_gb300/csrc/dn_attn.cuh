@@ -28,6 +28,13 @@ namespace dn {
 
 constexpr int kAttnSms = 152;  // GB300
 
+// 2^x within 2 units in the last place; results below 2^-126 are 0.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
 struct AttnArgs {
     KvPool p;
     const void *q;

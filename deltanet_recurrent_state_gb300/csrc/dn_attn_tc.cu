@@ -59,12 +59,6 @@ namespace {
 
 __device__ unsigned int g_attn_timeouts;
 
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
 // D += A B with A in tensor memory (16-bit elements, two to a column).
 __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc, bool acc) {
     asm volatile("{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
@@ -731,11 +725,11 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
                 const bool grew = big > m + 8.f;
                 const float base_old = m;
                 if (grew) m = big;
-                float f = grew ? ex2(base_old - m) : 1.f;
+                float f = grew ? exp2_fast(base_old - m) : 1.f;
                 const bool moved = KV8 && ref_now != ref;
                 if (__any_sync(0xffffffffu, grew) || moved) {
                     l *= f;
-                    if (moved) f *= ex2((float)(ref - ref_now));
+                    if (moved) f *= exp2_fast((float)(ref - ref_now));
                     ref = ref_now;
                     if (NS == 1) {  // the product of the step before may be under way
                         if (!wait_for(&bar.pv, (j - 1) & 1, abort)) { ok = false; break; }
@@ -768,7 +762,7 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
 #pragma unroll
                 for (int e = 0; e < 32; e += 2) {
                     float2 y = __ffma2_rn(make_float2(__uint_as_float(now[e]), __uint_as_float(now[e + 1])), f2, b2);
-                    y = make_float2(ex2(y.x), ex2(y.y));
+                    y = make_float2(exp2_fast(y.x), exp2_fast(y.y));
                     l2[(e >> 1) & 1] = __fadd2_rn(l2[(e >> 1) & 1], y);
                     p[e / 2] = pack2<MB>(y.x, y.y);
                 }
@@ -820,8 +814,8 @@ attn_tile_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ CUt
             const float2 y = ml[(1 - s) * 128 + row];
             top = fmaxf(m, y.x);
             const float base = top == -INFINITY ? 0.f : top;
-            f0 = ex2(m - base);
-            f1 = ex2(y.x - base);
+            f0 = exp2_fast(m - base);
+            f1 = exp2_fast(y.x - base);
             sum = s ? f1 * y.y + f0 * l : f0 * l + f1 * y.y;
             f0 *= up;
         }
