@@ -11,9 +11,9 @@
 // 16- or 32-token pieces of the range through a private ring in shared memory (cp.async, XOR-swizzled
 // chunks) and never waits for another warp until the end, where the warps' m, sums and outputs are
 // merged. Pages are multiples of 16 tokens, so 16 tokens are one contiguous segment of the pool.
-// Measured on a GB300: 64 single tokens over ragged caches of up to 8,000 bf16 tokens (8 x 4 heads of 128) 179 us,
-// 6.1 TB/s, 90 % of the copy rate; 64 blocks of 1 to 4 tokens over up to 25,000 in 8 bits 388 us, 5.0 TB/s (counters of
-// 24 such requests: ALU pipe 54 %, issue slots 39 %, 2.6 warps a scheduler). One token over 1,000 (24 x 256 heads) takes
+// Measured on a GB300: 64 single tokens over ragged caches of up to 8,000 bf16 tokens (8 x 4 heads of 128) 178 us,
+// 6.1 TB/s, 90 % of the copy rate; 64 blocks of 1 to 4 tokens over up to 25,000 in 8 bits 379 us, 5.1 TB/s (counters of
+// 24 such requests: ALU pipe 53 %, issue slots 39 %, 2.6 warps a scheduler). One token over 1,000 (24 x 256 heads) takes
 // about 9.8 us on the device for 0.6 us of bytes: latency.
 //
 // fp16 probabilities are held as 2^15 p, which fp16 has room for (p <= 1): those below 2^-39 are lost to the product with the

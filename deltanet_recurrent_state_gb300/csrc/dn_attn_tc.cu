@@ -34,12 +34,12 @@
 // sum at the end takes the factor out again. fp16 ones are held as 2^7 p, up to 2^15: fp16's smallest number is then
 // 2^-31 (see dn_attn.cu).
 //
-// Measured on a GB300. A prompt's chunk (2,048 tokens, 25,000 cached with them, 32 x 128 heads, bf16) takes 587 us,
+// Measured on a GB300. A prompt's chunk (2,048 tokens, 25,000 cached with them, 32 x 128 heads, bf16) takes 589 us,
 // 1,370 TFLOP/s, 71 % of cuBLAS's rate (about 565 back to back on one input): its 256 units are 1.7 waves of 152,
 // 84 % of two, and a chunk of 1,216 over 8,192 keeps the tensor pipe active 64 % of the cycles. A verify block
 // (96 rows of D = 256 over 25,000 tokens, 16 bits) takes 34 us for 15 us of bytes: one wave, of which about 8 us
-// are its end and the join. Over 268,000 tokens in 8 bits it takes 175 us for 81: a 64-token tile takes 2,750 to 3,300
-// cycles by clock stamps, 1,400 would be the copy rate; three 16-bit slots are what fits beside q.
+// are its end and the join. Over 268,000 tokens in 8 bits it takes 172 us for 81: a 64-token tile took 2,750 to 3,300
+// cycles by clock stamps at 175 us, 1,400 would be the copy rate; three 16-bit slots are what fits beside q.
 //
 // Every wait is bounded in time; a wait that runs out raises the CTA's abort flag, and every role
 // leaves after its own copies and products have landed.

@@ -8,8 +8,8 @@
 // the loads of all its passes issued before the first store. The row maximum that the 8-bit form
 // needs is a shuffle over the D / 8 lanes that hold the row. The request of a packed row is found by the
 // whole warp at once (32 entries of start a step), in the shadow of the data loads.
-// Measured on a GB300: 25,000 tokens of 8 x 128-wide heads from bf16 to 8 bits 27.5 us, 5.6 TB/s, 83 % of the copy rate;
-// 25,000 of 4 x 256 read back from 8 bits 26.2 us, 5.9 TB/s, 87 %. Small calls are latency.
+// Measured on a GB300: 25,000 tokens of 8 x 128-wide heads from bf16 to 8 bits 27.6 us, 5.6 TB/s, 82 % of the copy rate;
+// 25,000 of 4 x 256 read back from 8 bits 26.4 us, 5.8 TB/s, 86 %. Small calls are latency.
 #include <type_traits>
 
 #include <cuda_runtime.h>
