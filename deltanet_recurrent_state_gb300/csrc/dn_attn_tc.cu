@@ -19,8 +19,8 @@
 // descriptors read; the producer's lanes look the pages up 32 at a time. A page that a
 // request does not have is an out-of-range coordinate, which the copy fills with zeros. Rows of the last
 // page past the range, and of the first one before a window, may hold anything: their scores are masked, and
-// their values are zeroed in shared memory before the product (0 x NaN is not 0). q comes the same way, G heads by 128 / G tokens a
-// box, so a tile is as many whole tokens as 128 rows hold.
+// their values are zeroed in shared memory before the product (0 x NaN is not 0). q comes the same way, G heads
+// by 128 / G tokens a box, so a tile is as many whole tokens as 128 rows hold.
 //
 // 8-bit caches. The boxes land in a ring of raw tiles, and a warpgroup turns them into fp16 tiles, multiplied
 // by the powers of two 2^(E - R + 7) of the tokens: R is the tile's largest exponent for the keys, whose
