@@ -236,8 +236,10 @@ extern "C" dn_status dn_rope_append(int B, int total, int heads, int group, int 
     if (!kv_dtypes_known(io_dt, cache_dt)) return DN_ERR_INVALID_ARG;
     if (!kv_shape_ok(D, page) || !kv_dtypes_ok(io_dt, cache_dt)) return DN_ERR_UNSUPPORTED;
     if (rot < 16 || rot > D || rot % 16) return DN_ERR_UNSUPPORTED;
-    const int64_t wide_k = (int64_t)heads * D, wide_q = wide_k * group;
-    if (wide_q > (1 << 24) || !kv_pages_ok(max_pages, pages, page)) return DN_ERR_INVALID_ARG;
+    const int64_t wide_k = (int64_t)heads * D;
+    // (the product of all three is taken only where it is known to fit)
+    if (wide_k > (1 << 24) || group > (1 << 24) / wide_k || !kv_pages_ok(max_pages, pages, page)) return DN_ERR_INVALID_ARG;
+    const int64_t wide_q = wide_k * group;
     if (q_stride < wide_q || k_stride < wide_k || v_stride < wide_k || (q_stride | k_stride | v_stride) % 8) return DN_ERR_INVALID_ARG;
     if (!(amplitude > 0.f) || !(amplitude < 3e38f) || !q_weight != !k_weight || (q_weight && (!(eps > 0.f) || !(eps < 3e38f)))) return DN_ERR_INVALID_ARG;
     // a warp's number fits 32 bits even where each has one pass

@@ -76,6 +76,17 @@ def test_rope_append_rejects(lib, over, want):
     assert lib.dn_rope_append(*filled(ROPE, over)) == want
 
 
+@pytest.mark.parametrize("over", [
+    dict(heads=1 << 30, D=256, rot=256, group=(1 << 26) - 2, qs=1 << 40, ks=1 << 40, vs=1 << 40),
+    dict(heads=1 << 30, D=256, rot=256, group=1 << 26, qs=0, ks=1 << 38, vs=1 << 38),
+    dict(heads=(1 << 31) - 1, group=(1 << 31) - 1, qs=1 << 62, ks=1 << 62, vs=1 << 62), dict(heads=1 << 19, group=1, qs=1 << 25, ks=1 << 25, vs=1 << 25),
+    dict(heads=1 << 9, group=1 << 10, qs=1 << 25, ks=1 << 15, vs=1 << 15)])
+def test_rope_append_rejects_products_of_heads_past_its_bound(lib, over):
+    """heads * group * D > 2^24, also where that product or the number of warps is small modulo 2^64."""
+    for total in (1, 2):
+        assert lib.dn_rope_append(*filled(ROPE, dict(over, total=total))) == INVALID
+
+
 def test_rope_append_of_nothing(lib):
     assert lib.dn_rope_append(*filled(ROPE, dict(total=0))) == OK
     assert lib.dn_rope_append(*filled(ROPE, dict(B=0))) == OK
