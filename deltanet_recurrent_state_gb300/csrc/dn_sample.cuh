@@ -1032,6 +1032,9 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
     }
     if (floor > tau1) {
         tau1 = floor == 0.f ? -1.4e-45f : __uint_as_float(__float_as_uint(floor) + (floor > 0.f ? -1 : 1));  // the float below
+        // and the type's value there or below it: a negative float between two values has the key of the upper one, which may be kept
+        const unsigned key = key_of<E>(tau1);
+        tau1 = value_of<E>(value_of<E>(key) > tau1 ? key - 1 : key);
         r1 = 0;
     }
 
@@ -1077,7 +1080,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
     u64 kept, kept_before, all_kept, tau_weight, tail;  // this warp's, of the warps before it, of the row; of a token at tau
     unsigned alike, alike_before, r;
     auto above_tau = [&](float x) { return x > tau; };
-    unsigned lo = key_of<E>(tau1), hi = key_of<E>(top);
+    unsigned lo = key_of<E>(tau1), hi = key_of<E>(top), now = key_of<E>(tau);  // tau's key is now, and in the end one of lo .. hi
     for (;;) {
         for (int tries = 0;; ++tries) {
             Mass m = {};
@@ -1135,38 +1138,36 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
             if (!(p < 1.f)) break;
             if (r1) all += (u64)r1 * weight_at<kShort>(tau1, scale, s.powers);
             const u64 goal = nucleus(all);
-            if (all_kept >= goal) {
-                lo = key_of<E>(tau) + 1;  // fewer: tau is higher
-            } else if (all_kept + (u64)r * tau_weight < goal) {
-                hi = key_of<E>(tau) - 1;
-            } else {
+            const bool more = all_kept >= goal, fewer = all_kept + (u64)r * tau_weight < goal;  // tau is higher, or lower
+            if (!more && !fewer) {
                 r = (unsigned)((goal - all_kept + tau_weight - 1) / tau_weight);
                 break;
             }
-            if (lo >= hi) {
-                tau = fmaxf(value_of<E>(lo), tau1);
-                if (tries > 60) break;
-                continue;
+            if (more) lo = now + 1;
+            else hi = now - 1;
+            // No value is left where the sum over a value's tokens and their number times one's weight, which differ by some units, lie on
+            // either side of the goal: then all of them are kept and none below. (And 16 growing steps and 32 halvings are not passed.)
+            if (lo > hi || tries > 60) {
+                if (more) r = 0;
+                break;
             }
             // the next value in the bin, at first; then in steps that grow, to the middle of what is left at most
-            unsigned next = 0;
-            if (tries < 3 && listed > 0) {
-                const unsigned now = key_of<E>(tau);
-                const bool up = lo > now;
-                unsigned best = up ? 0xffffffffu : 0u;
+            unsigned next = lo == hi ? lo : 0;
+            if (!next && tries < 3 && listed > 0) {
+                unsigned best = more ? 0xffffffffu : 0u;
                 for (int j = lane; j < listed; j += 32) {
                     const unsigned key = s.merged[j];
-                    if (up ? key > now : key < now) best = up ? min(best, key) : max(best, key);
+                    if (more ? key > now : key < now) best = more ? min(best, key) : max(best, key);
                 }
-                best = up ? __reduce_min_sync(0xffffffffu, best) : __reduce_max_sync(0xffffffffu, best);
+                best = more ? __reduce_min_sync(0xffffffffu, best) : __reduce_max_sync(0xffffffffu, best);
                 if (best >= lo && best <= hi) next = best;
             }
             if (!next) {
                 const unsigned step = min((hi - lo) / 2, tries < 16 ? (1u << 2 * tries) - 1u : 0xffffffffu);
-                next = lo > key_of<E>(tau) ? lo + step : hi - step;
+                next = more ? lo + step : hi - step;
             }
-            tau = fmaxf(value_of<E>(next), tau1);
-            if (tries > 60) break;  // (never: 16 such steps and 32 halvings end it)
+            now = next;
+            tau = fmaxf(value_of<E>(now), tau1);
         }
 
         // ---- the token: the first at which the kept mass passes u times the total ----

@@ -1,0 +1,105 @@
+"""dn_accept_sampled where sums over a row decide: rows of a few distinct values, whose 64-bit sums are products and so known to 10^-15,
+and random numbers a few 10^-11 beside a border of the running sum.
+
+A weight is right to 2^-33 of itself. A share of a sum changes by its two sides' product, at most 1/4, times the difference of
+their errors, at most 2^-32: 2^-34. Sums are taken in units of 2^-43 of the largest weight, with half a unit for each of 128
+warps, twice: 2^-36. So a random number lies within the interval of its token, widened by 2^-34 + 2^-36 on either side (`TOL`, 7.3e-11).
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from deltanet_recurrent_state_gb300 import binding as dn
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
+TOL = 2.0 ** -34 + 2.0 ** -36
+
+
+def value(x, dt):
+    """x as the type holds it."""
+    return float(torch.tensor(x, dtype=torch.float64).to(DT[dt]))
+
+
+def weight(x, top, temperature):
+    return np.exp((np.float64(x) - top) / np.float64(np.float32(temperature)))
+
+
+def draw(logits, u, temperature, top_k=0, top_p=1.0, min_p=0.0, workspace=None):
+    """Targets of rows [B, V]; the parameters are a row's each, or all rows'."""
+    B = logits.shape[0]
+
+    def column(v, dtype):
+        return torch.as_tensor(np.broadcast_to(np.asarray(v), (B,)).copy()).to(dtype).cuda()
+
+    got = dn.dn_accept_sampled(logits[:, None].cuda(), torch.zeros((B, 1), dtype=torch.int32, device="cuda"), column(u, torch.float32)[:, None],
+                               column(temperature, torch.float32), column(top_k, torch.int32), column(top_p, torch.float32),
+                               column(min_p, torch.float32), workspace=workspace)
+    return got[0][:, 0].cpu().numpy()
+
+
+# ---- a top_p whose border lies beside the least value that min_p keeps, and one between two values ----
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("B", [12, 100])
+def test_top_p_reaches_the_least_value_that_min_p_keeps(cuda, B, dt):
+    """Many tokens at the least kept value, below zero, a floor that is no value of the type, and a top_p that keeps all that min_p does."""
+    V = 24000
+    g = torch.Generator().manual_seed(B)
+    logits = torch.empty((B, V), dtype=DT[dt])
+    min_p = []
+    for b in range(B):
+        top = value(-0.25 - 0.5 * b / B, dt)
+        least = value(top - 1.0, dt)
+        logits[b] = (top - 1.0 * torch.rand(V, generator=g, dtype=torch.float64) ** 2).clamp(least, top).to(DT[dt])
+        logits[b, torch.randint(0, V, (6000,), generator=g)] = least
+        logits[b, torch.randint(0, V, (6000,), generator=g)] = least - 1.0  # (min_p leaves these out)
+        logits[b, b] = top
+        min_p.append(float(np.float32(weight(least, top, 1.0) * (1 - 1e-4))))
+    u = (np.arange(B) + 0.5) / B
+    for top_p in (1 - 2.0 ** -24, 1 - 2.0 ** -23):
+        ws = dn.sample_workspace(B, 1, V, cuda)
+        token = draw(logits, u, 1.0, 0, top_p, min_p, workspace=ws)
+        assert int(ws.count_nonzero()) == 0
+        for b in range(B):
+            x = logits[b].double().numpy()
+            w = np.exp(x - x.max())
+            w[w < min_p[b]] = 0.0
+            assert w[w > 0].min() > 4 * 2.0 ** -23 * w.sum()  # (the last token is more than what top_p leaves out)
+            upto = np.cumsum(w) / w.sum()
+            i = int(token[b])
+            assert w[i] > 0 and upto[i] - w[i] / w.sum() - TOL <= float(np.float32(u[b])) <= upto[i] + TOL, (top_p, b, i)
+
+
+@pytest.mark.parametrize("dt", list(DT))
+def test_top_p_between_two_values(cuda, dt):
+    """The mass down to a value is top_p's to a few 10^-10, closer than sums of the value's tokens in 32 bits come to their number times one of them."""
+    top, n2 = value(9.0, dt), 3000
+    one, two = value(top - 10.0, dt), value(top - 10.5, dt)
+    w, w2 = weight(one, top, 1.0), weight(two, top, 1.0)
+    cases = []
+    for n in range(4000, 9000):
+        share = (1 + n * w) / (1 + n * w + n2 * w2)
+        p = np.float32(share)
+        for q in (p, np.nextafter(p, np.float32(0)), np.nextafter(p, np.float32(1))):
+            if 1e-10 < abs(float(q) - share) < 2e-9:
+                cases.append((n, float(q), share))
+    assert len(cases) >= 40
+    cases = cases[:: max(1, len(cases) // 120)][:120]
+    V = 12100
+    logits = torch.full((len(cases), V), -float("inf"), dtype=DT[dt])
+    u = np.float32(1 - 2.0 ** -24)
+    for b, (n, _, _) in enumerate(cases):
+        logits[b, :n2] = two
+        logits[b, n2:n2 + n] = one
+        logits[b, n2 + n] = top
+    # the peak is the last: its border tells what is kept before it
+    token = draw(logits, [0.0 if b % 2 else u for b in range(len(cases))], 1.0, 0, [c[1] for c in cases])
+    for b, (n, p, share) in enumerate(cases):
+        if b % 2:  # u = 0: the first kept token
+            assert token[b] == (0 if p > share else n2), (b, n, p - share)
+        else:
+            assert token[b] == n2 + n, b
