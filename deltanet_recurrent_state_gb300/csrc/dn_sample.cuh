@@ -21,10 +21,11 @@
 // Calls of many rows leave rows that need several such passes to a second kernel with eight CTAs for each of them.
 //
 // Exact masses. Which token a random number means is decided by sums over the vocabulary against borders that lie as dense as
-// its tokens, so weights are taken to 2^-36 of themselves (a pair of floats: reduced argument, table, short series) and summed
-// on a fixed grid of 2^-43 of the largest, where the order of a sum does not matter. 32-bit arithmetic would give another
+// its tokens, so weights are taken to 2^-33 of themselves, 2^-36.7 in the mean square (a pair of floats: reduced argument, table, short
+// series; P. T. P. Tang, "Table-driven implementation of the exponential function in IEEE floating-point arithmetic", 1989), and
+// summed on fixed grids, 2^-43 of the largest over a row, where the order of a sum does not matter. 32-bit arithmetic would give another
 // token than 64 bits do for one random number in some thousands over a flat row; this does for one in 10^7.
-// That costs some 57 issue slots a token, and 32-bit arithmetic 13. So tokens of less than 2^-14 of the largest weight are summed in
+// That costs some 59 issue slots a token, and 32-bit arithmetic 13. So tokens of less than 2^-14 of the largest weight are summed in
 // 32 bits at first. Where they make up less than 2^-10 of the row, their errors, of either sign and some 2^-21 each over
 // thousands of tokens, leave the sums right to 2^-36 as well; else (and near the maximum always) the result
 // counts only if no border lies within their error's bound, and the row is summed again exactly if one does.
@@ -70,7 +71,9 @@ constexpr float kTail = 14.f;        // the negative binary logarithm of a weigh
 constexpr int kTailShift = 10;       // all of those make up much of a row from 2^-10 of it on
 constexpr int kTailError = 16;       // and their sum is off by less than 2^-16: y by 2^-22.7 of itself (at 44, beyond which weights are below
                                      // the grid, 2^-17.7 of the weight), the exponential by 2^-22, a sum of 32 by 2^-19
-constexpr int kFixed = 43;           // weights are summed in units of 2^-43 of the largest
+constexpr int kFixed = 43;           // sums over a row are in units of 2^-43 of the largest weight: 2^19 of them fit 64 bits
+constexpr int kList = 50;            // over listed tokens, and a warp's tokens: units of 2^-50, 12,500 tokens
+constexpr int kFine = 56;            // a token's own weight, and what a warp adds up below the units of a row: 2^-56
 constexpr float kCountScale = 32.f;  // bins a unit of distance, for counts
 
 // kAll: a kernel for all that a row may need. kEasy leaves rows that take several passes over all of their tokens to kHard, which
@@ -189,7 +192,7 @@ struct Shared {
     };
 };
 
-// The weights of two tokens, each as a sum of two floats right to 2^-36 of itself. y = n + j / 16 + f with |f| <= 1/32; all in packed
+// The weights of two tokens, each as a sum of two floats right to 2^-33 of itself. y = n + j / 16 + f with |f| <= 1/32; all in packed
 // arithmetic, two tokens an instruction, with no sign to change on the way.
 struct Weights {
     float2 hi, lo;
@@ -222,24 +225,43 @@ __device__ __forceinline__ Weights weights_of(float x0, float x1, const Scale &c
     return Weights{__fmul2_rn(hi, power), __fmul2_rn(lo, power)};
 }
 
-// Two sums of up to 32 weights each: the parts on a grid of 2^-18 add up exactly in a float, and the others are small.
+// Two sums of up to 32 weights each. Parts on grids of 2^-18 and 2^-37 add up exactly in floats; the rest, of 2^-38 and 2^-25 of the weight at most, has
+// an error of 2^-45 of the weights. (Equal tokens round alike, so a plain float sum of them is off by up to 2^-20 of itself however many lanes share it.)
 struct Sum {
-    float2 a = {0.f, 0.f}, b = {0.f, 0.f};
+    float2 a = {0.f, 0.f}, b = {0.f, 0.f}, c = {0.f, 0.f};
     __device__ __forceinline__ void add(const Weights &w, bool first, bool second) {
         const float2 hi = make_float2(first ? w.hi.x : 0.f, second ? w.hi.y : 0.f), lo = make_float2(first ? w.lo.x : 0.f, second ? w.lo.y : 0.f);
-        const float2 on = __fadd2_rn(__fadd2_rn(__fadd2_rn(hi, lo), two(48.f)), two(-48.f));  // the floats of 32 .. 64 have steps of 2^-18
+        const float2 on = __fadd2_rn(__fadd2_rn(hi, two(48.f)), two(-48.f));  // the floats of 32 .. 64 have steps of 2^-18
+        const float2 rest = __ffma2_rn(on, two(-1.f), hi);                    // (exact)
+        const float2 mid = __fadd2_rn(__fadd2_rn(rest, two(0x1.8p-14f)), two(-0x1.8p-14f));  // those of 2^-14 .. 2^-13 of 2^-37
         a = __fadd2_rn(a, on);
-        b = __fadd2_rn(b, __fadd2_rn(__ffma2_rn(on, two(-1.f), hi), lo));
+        b = __fadd2_rn(b, mid);
+        c = __fadd2_rn(c, __fadd2_rn(__ffma2_rn(mid, two(-1.f), rest), lo));
     }
-    __device__ __forceinline__ u64 fixed() const {
-        return ((u64)(long long)__float2int_rn((a.x + a.y) * 0x1p18f) << (kFixed - 18)) + (u64)(long long)__float2int_rn(b.x * 0x1p43f) +
-               (u64)(long long)__float2int_rn(b.y * 0x1p43f);
+    __device__ __forceinline__ u64 fixed() const {  // the parts on the grids, in units of 2^-kFixed (the two sums' sums are of 24 bits)
+        return ((u64)(long long)__float2int_rn((a.x + a.y) * 0x1p18f) << (kFixed - 18)) +
+               ((u64)(long long)__float2int_rn((b.x + b.y) * 0x1p37f) << (kFixed - 37));
     }
+    // the rest, in units of 2^-kFine, and a sum of light tokens
+    __device__ __forceinline__ long long fine(float2 light) const { return __float2ll_rn(((c.x + c.y) + (light.x + light.y)) * 0x1p56f); }
 };
-__device__ __forceinline__ u64 weight_of(float x, const Scale &c, const float2 *powers) {  // one token's, in units
+__device__ __forceinline__ u64 weight_of(float x, const Scale &c, const float2 *powers) {  // one token's, in units of 2^-kFine
     Sum s;
     s.add(weights_of(x, x, c, powers), true, false);
-    return s.fixed();
+    return (s.fixed() << (kFine - kFixed)) + (u64)s.fine(two(0.f));
+}
+// Units of 2^-kFine as coarser ones of 2^-bits.
+__device__ __forceinline__ u64 coarser(u64 fine, int bits) { return (fine + (1ull << (kFine - bits - 1))) >> (kFine - bits); }
+__device__ __forceinline__ u64 rest_of(long long fine) { return (u64)((fine + (1ll << (kFine - kFixed - 1))) >> (kFine - kFixed)); }  // (below 0, too)
+// The mass of n tokens alike, rounded down to units of 2^-kFixed, and the fewest of them with a mass of `need` (above 0; enough of them have it).
+__device__ __forceinline__ u64 mass_of(unsigned n, u64 weight) {
+    return (__umul64hi(n, weight) << (64 - kFine + kFixed)) | (n * weight >> (kFine - kFixed));
+}
+__device__ __forceinline__ unsigned fewest_of(u64 need, u64 weight) {
+    unsigned n = (unsigned)((double)need * (double)(1 << (kFine - kFixed)) / (double)weight);  // off by one at most
+    while (mass_of(n, weight) < need) ++n;
+    while (n > 0 && mass_of(n - 1, weight) >= need) --n;
+    return n;
 }
 
 static __device__ __noinline__ u64 weight_called(float x, Scale c, const float2 *powers) { return weight_of(x, c, powers); }
@@ -632,7 +654,16 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
         Sum exact, exact_above;
         float2 small, small_above;
         int n;
-        u64 all, kept, tail;
+        u64 all, kept;
+        long long rest, rest_kept;  // (light tokens, and what lies below the units, of all and of those above)
+    };
+    auto flush_mass = [&](auto both, Mass &m) {
+        m.all += m.exact.fixed();
+        m.rest += m.exact.fine(m.small);
+        if (decltype(both)::value) {
+            m.kept += m.exact_above.fixed();
+            m.rest_kept += m.exact_above.fine(m.small_above);
+        }
     };
     auto add_mass = [&](auto both, auto unroll, Mass &m, uint4 u, auto in, auto above, bool all_exact) {
         constexpr bool BOTH = decltype(both)::value;
@@ -656,23 +687,24 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
             }
         }
         if ((m.n += VEC) == 64) {
-            m.tail += __float2ull_rn((m.small.x + m.small.y) * 0x1p43f);
-            m.small = two(0.f);
-            m.all += m.exact.fixed();
-            m.exact = Sum();
-            if (BOTH) {
-                m.kept += m.exact_above.fixed() + __float2ull_rn((m.small_above.x + m.small_above.y) * 0x1p43f);
-                m.small_above = two(0.f);
-                m.exact_above = Sum();
-            }
+            flush_mass(both, m);
+            m.exact = m.exact_above = Sum();
+            m.small = m.small_above = two(0.f);
             m.n = 0;
         }
     };
-    auto end_mass = [&](auto both, Mass &m) {  // returns the tail
-        const u64 tail = m.tail + __float2ull_rn((m.small.x + m.small.y) * 0x1p43f);
-        m.all += m.exact.fixed() + tail;
-        if (decltype(both)::value) m.kept += m.exact_above.fixed() + __float2ull_rn((m.small_above.x + m.small_above.y) * 0x1p43f);
-        return tail;
+    // The warp's mass of its lanes', and that of its light tokens.
+    auto end_mass = [&](auto both, Mass &m, bool all_exact, u64 &tail) {
+        flush_mass(both, m);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            m.all += __shfl_xor_sync(0xffffffffu, m.all, off), m.rest += __shfl_xor_sync(0xffffffffu, m.rest, off);
+            if (decltype(both)::value) m.kept += __shfl_xor_sync(0xffffffffu, m.kept, off), m.rest_kept += __shfl_xor_sync(0xffffffffu, m.rest_kept, off);
+        }
+        const u64 rest = rest_of(m.rest);
+        m.all += rest;
+        if (decltype(both)::value) m.kept += rest_of(m.rest_kept);
+        tail = all_exact || m.rest < 0 ? 0 : rest;
     };
     const std::true_type both{};
     const std::false_type one{};
@@ -686,8 +718,8 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
         bool part;
         return !(uniform > 0.f) ? 0 : uniform < 1.f ? part_of(all, uniform, part) : all - 1;
     };
-    auto log_share = [&](float x, u64 all) {  // of a token's weight in the kept mass, which is 1 or more
-        const float over = __ull2float_rn(all - (1ull << kFixed)) * 0x1p-43f;
+    auto log_share = [&](float x, u64 all, int bits) {  // of a token's weight in the kept mass, which is 1 or more, in units of 2^-bits
+        const float over = __ull2float_rn(all - (1ull << bits)) * __int_as_float((127 - bits) << 23);
         return (x == top ? 0.f : (x - top) / temp) - log1pf(over);
     };
 
@@ -708,11 +740,8 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
         if (whole) {
             Mass m = {};
             each_vector([&](uint4 u) { add_mass(one, pairs, m, u, [&](float x) { return x >= lowest; }, [](float) { return true; }, false); });
-            tail = end_mass(one, m);
-            all = m.all;
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) all += __shfl_xor_sync(0xffffffffu, all, off), tail += __shfl_xor_sync(0xffffffffu, tail, off);
-            if (lane == 0) s.scan64[warp] = all, s.scan64b[warp] = tail;
+            end_mass(one, m, false, tail);
+            if (lane == 0) s.scan64[warp] = m.all, s.scan64b[warp] = tail;
         }
         __syncthreads();
         if (lane == 0) s.scan32[warp] = found;
@@ -839,9 +868,10 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
                 return true;
             }
             const u64 error = tail >> kTailError, goal = nucleus(all), most = nucleus(all + error);
+            mass >>= kList - kFixed;  // (a goal of whole units is reached or not)
             const bool doubt = keep && (mass >= nucleus(all - error)) != (mass >= most);
             if (keep && mass >= goal) keep = 0;
-            return !__syncthreads_or(doubt) && most <= sum;
+            return !__syncthreads_or(doubt) && most <= sum >> (kList - kFixed);
         };
         if (fits) {
             if (rank == 0) {
@@ -851,7 +881,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
                     for (int i = 1; i < kMaxCluster; ++i)
                         if (i < ranks && j >= starts[i]) owner = i, start = starts[i];
                     const uint2 e = *cluster.map_shared_rank(&s.near[j - start], owner);
-                    entry[j] = Entry{e.x, (int)e.y, k == 1 ? 1ull << kFixed : weight_of(value_of<E>(e.x), scale, s.powers)};
+                    entry[j] = Entry{e.x, (int)e.y, k == 1 ? 1ull << kList : coarser(weight_of(value_of<E>(e.x), scale, s.powers), kList)};
                 }
                 __syncthreads();
                 if (whole) {
@@ -986,7 +1016,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
             }
             token = __shfl_sync(0xffffffffu, token, __ffs(here) - 1);
             token_key = __shfl_sync(0xffffffffu, token_key, __ffs(here) - 1);
-            finish(token, lane == 0 ? log_share(value_of<E>(token_key), total) : 0.f);
+            finish(token, lane == 0 ? log_share(value_of<E>(token_key), total, kList) : 0.f);
             return;
         }
     }
@@ -1058,7 +1088,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
         __syncthreads();
         sum = 0.f;
         for (int w = 0; w < kWarps; ++w) sum += s.scanf[w];
-        if (r1) sum += (float)r1 * ((float)weight_at<kShort>(tau1, scale, s.powers) * (0x1p-43f * 32768.f));
+        if (r1) sum += (float)r1 * ((float)weight_at<kShort>(tau1, scale, s.powers) * (0x1p-56f * 32768.f));
         __syncthreads();
         const float goal = p * sum;
         find_bin<kShort>(s, 0.f, goal, v0, v1);
@@ -1077,7 +1107,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
 
     // ---- the exact masses, and what top_p keeps ----
     bool heavy;  // the light tokens, in 32 bits, make up much of the row
-    u64 kept, kept_before, all_kept, tau_weight, tail;  // this warp's, of the warps before it, of the row; of a token at tau
+    u64 kept, kept_before, all_kept, tau_weight, tail;  // this warp's, of the warps before it, of the row; of a token at tau (2^-kFine)
     unsigned alike, alike_before, r;
     auto above_tau = [&](float x) { return x > tau; };
     unsigned lo = key_of<E>(tau1), hi = key_of<E>(top), now = key_of<E>(tau);  // tau's key is now, and in the end one of lo .. hi
@@ -1088,17 +1118,12 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
             u64 mine;  // of all that count, with a top_p
             if (p < 1.f) {
                 each_vector([&](uint4 u) { add_mass(both, pairs, m, u, [&](float x) { alike += x == tau; return x > tau1; }, above_tau, all_exact); });
-                tail = end_mass(both, m);
+                end_mass(both, m, all_exact, tail);
                 mine = m.all, kept = m.kept;
             } else {
                 each_vector([&](uint4 u) { add_mass(one, pairs, m, u, [&](float x) { alike += x == tau; return x > tau; }, above_tau, all_exact); });
-                tail = end_mass(one, m);
+                end_mass(one, m, all_exact, tail);
                 mine = kept = m.all;
-            }
-#pragma unroll
-            for (int off = 16; off > 0; off >>= 1) {
-                mine += __shfl_xor_sync(0xffffffffu, mine, off), tail += __shfl_xor_sync(0xffffffffu, tail, off);
-                kept += __shfl_xor_sync(0xffffffffu, kept, off);
             }
             alike = __reduce_add_sync(0xffffffffu, alike);
             __syncthreads();
@@ -1136,11 +1161,11 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
             tau_weight = weight_at<kShort>(tau, scale, s.powers);
             r = tau > tau1 ? all_alike : r1;  // tokens at tau that may be kept
             if (!(p < 1.f)) break;
-            if (r1) all += (u64)r1 * weight_at<kShort>(tau1, scale, s.powers);
+            if (r1) all += mass_of(r1, weight_at<kShort>(tau1, scale, s.powers));
             const u64 goal = nucleus(all);
-            const bool more = all_kept >= goal, fewer = all_kept + (u64)r * tau_weight < goal;  // tau is higher, or lower
+            const bool more = all_kept >= goal, fewer = all_kept + mass_of(r, tau_weight) < goal;  // tau is higher, or lower
             if (!more && !fewer) {
-                r = (unsigned)((goal - all_kept + tau_weight - 1) / tau_weight);
+                r = fewest_of(goal - all_kept, tau_weight);
                 break;
             }
             if (more) lo = now + 1;
@@ -1171,8 +1196,8 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
         }
 
         // ---- the token: the first at which the kept mass passes u times the total ----
-        const u64 all = all_kept + (u64)r * tau_weight, goal = draw(all);
-        auto mass = [&](u64 m, unsigned alike_upto) { return m + (u64)min(alike_upto, r) * tau_weight; };
+        const u64 all = all_kept + mass_of(r, tau_weight), goal = draw(all);
+        auto mass = [&](u64 m, unsigned alike_upto) { return m + mass_of(min(alike_upto, r), tau_weight); };
         // the warp that has it; then its steps, which all warps share
         if (threadIdx.x == 0) s.chosen = s.place = -1;
         __syncthreads();
@@ -1196,9 +1221,8 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
                     Mass m = {};
                     unsigned same = 0, some = 0;
                     if (i < end) add_mass(one, pairs, m, fetch(i), [&](float x) { same += x == tau; some += x > tau; return x > tau; }, above_tau, all_exact);
-                    end_mass(one, m);
-#pragma unroll
-                    for (int off = 16; off > 0; off >>= 1) m.all += __shfl_xor_sync(0xffffffffu, m.all, off);
+                    u64 light;
+                    end_mass(one, m, true, light);
                     same = __reduce_add_sync(0xffffffffu, same);
                     some = __reduce_add_sync(0xffffffffu, some);
                     if (lane == 0) s.step_mass[step] = m.all, s.step_alike[step] = same, s.step_kept[step] = some;
@@ -1221,6 +1245,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
             int mine = -1;
             float mine_x = top;
             bool clear_of = false;
+            u64 listed_upto = 0;  // of the tokens so far, in units of 2^-kList
             const u64 error = heavy ? tail >> (kTailError - 1) : 0;  // of the running mass and of the total
             for (int v = begin; v < end; v += kThreads / VEC) {
                 const int i = v + (int)threadIdx.x / VEC;
@@ -1229,7 +1254,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
                     const float2 pair = pair_of<E>(fetch(i), (int)threadIdx.x % VEC / 2);
                     x = threadIdx.x % 2 ? pair.y : pair.x;
                 }
-                const u64 w = x > tau ? weight_at<kShort>(x, scale, s.powers) : 0;
+                const u64 w = x > tau ? coarser(weight_at<kShort>(x, scale, s.powers), kList) : 0;
                 const unsigned equal = __ballot_sync(0xffffffffu, x == tau);
                 u64 upto = w;
 #pragma unroll
@@ -1239,14 +1264,15 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
                 }
                 if (lane == 31) s.scan64b[warp] = upto, s.scan32b[warp] = __popc(equal);
                 __syncthreads();
-                u64 kept_at = upto - w;
+                u64 listed_at = upto - w;
                 unsigned alike_at = __popc(equal & ((1u << lane) - 1u));
 #pragma unroll 1
                 for (int o = 0; o < kWarps; ++o) {
-                    if (o == warp) kept_at += kept_upto, alike_at += alike_upto;
-                    kept_upto += s.scan64b[o], alike_upto += s.scan32b[o];
+                    if (o == warp) listed_at += listed_upto, alike_at += alike_upto;
+                    listed_upto += s.scan64b[o], alike_upto += s.scan32b[o];
                 }
-                const u64 before = mass(kept_at, alike_at), after = mass(kept_at + w, alike_at + (x == tau));
+                const u64 before = mass(kept_upto + (listed_at >> (kList - kFixed)), alike_at);
+                const u64 after = mass(kept_upto + ((listed_at + w) >> (kList - kFixed)), alike_at + (x == tau));
                 int at = -1;
                 if (x > tau || (x == tau && alike_at < r)) {
                     at = mine = i * VEC + (int)threadIdx.x % VEC;
@@ -1282,7 +1308,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
                 continue;
             }
         }
-        if (token >= 0) finish(token, lane == 0 ? log_share(token_x, all) : 0.f);
+        if (token >= 0) finish(token, lane == 0 ? log_share(token_x, all, kFixed) : 0.f);
         return;
     }
 }

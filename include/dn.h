@@ -532,8 +532,8 @@ unsigned int dn_attn_wait_timeouts(void);
  *   workspace     >= dn_sample_workspace_bytes(B, T, V) bytes, 16-byte aligned, zeros before its first use; every call leaves it all
  *                 zeros again, also for calls of other sizes. Calls that may run concurrently need separate workspaces.
  *   V <= DN_SAMPLE_MAX_VOCAB (else DN_ERR_UNSUPPORTED); B * T < 2^28
- * Weights are kept to 2^-36 of themselves and summed in units of 2^-43 of the largest, so the target is that of a 64-bit
- * computation unless u (or top_p) is within some 10^-11 of a border. Results repeat bit for bit.
+ * Weights are right to 2^-33 of themselves and summed in units of 2^-43 of the largest, so the target is that of a 64-bit
+ * computation unless u (or top_p) is within 8 * 10^-11 of a border. Results repeat bit for bit.
  */
 #define DN_SAMPLE_MAX_VOCAB 400000
 size_t dn_sample_workspace_bytes(int B, int T, int V);

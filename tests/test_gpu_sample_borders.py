@@ -103,3 +103,72 @@ def test_top_p_between_two_values(cuda, dt):
             assert token[b] == (0 if p > share else n2), (b, n, p - share)
         else:
             assert token[b] == n2 + n, b
+
+
+# ---- light tokens that make up much of the row, and many equal ones far below the largest ----
+
+
+def beside_borders(borders, count, least=1.25 * TOL, most=5e-10):
+    """Random numbers, as 32-bit floats hold them, that lie beside a border and further than TOL from it."""
+    near = (borders[:, None] + np.array([-2.6, -1.6, -1.1, 1.1, 1.6, 2.6]) * 1e-10).astype(np.float32).astype(np.float64)
+    off = np.abs(near - borders[:, None])
+    out = np.unique(near[(off > least) & (off < most) & (near > 0) & (near < 1)])
+    return out[:: max(1, len(out) // count)][:count]
+
+
+def equal_light_rows(dt, top, low, temperature, n, peak_at, count):
+    """The borders of a row with a peak at place peak_at among n equal tokens, and random numbers beside them."""
+    w = weight(low, top, temperature)
+    upto = np.arange(1, n + 2) * w + np.where(np.arange(n + 1) >= peak_at, 1 - w, 0.0)  # mass of tokens 0 .. i
+    borders = upto / upto[-1]
+    return borders, beside_borders(borders[:-1], count)
+
+
+def check_equal_light(cuda, dt, V, top, low, temperature, n, peak_at, rows):
+    borders, chosen = equal_light_rows(dt, top, low, temperature, n, peak_at, rows)
+    assert len(chosen) >= min(rows, 20), len(chosen)
+    row = torch.full((V,), -float("inf"), dtype=DT[dt])
+    row[: n + 1] = low
+    row[peak_at] = top
+    u = chosen
+    want = np.searchsorted(borders, u, side="right")  # the first token whose border is above u
+    for batch in (len(u), 6):  # rows that fill the GPU, and a few
+        token = draw(row[None].expand(batch, V).contiguous(), u[:batch], temperature)
+        bad = token != want[:batch]
+        assert not bad.any(), (temperature, n, peak_at, bad.sum(), token[bad][:5], want[:batch][bad][:5])
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("share", [0.3, 0.02])
+@pytest.mark.parametrize("temperature", [1.0, 1.37])
+def test_many_equal_tokens_beside_a_peak(cuda, temperature, share, dt):
+    """Equal tokens lose as much, each, in a sum of 32 bits."""
+    V, top = 151936, 6.0
+    for n, peak_at in ((150000, 150000), (131000, 70000), (90001, 45000)):
+        low = value(top + temperature * np.log(share / n), dt)
+        check_equal_light(cuda, dt, V, top, low, temperature, n, peak_at, 100)
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("far", [37.3, 39.4, 40.6, 42.2, 44.5])
+def test_ties_far_below_the_largest(cuda, far, dt):
+    """top_k cuts through equal tokens of less than a unit of the sums: 10,000 and more of them, and their mass is counted to less than a unit each."""
+    V = 120000
+    top = 20.0
+    low = value(top - far * np.log(2.0), dt)
+    w = weight(low, top, 1.0)
+    for B in (4, 100):
+        top_k = [1 + (110000, 40000, 10001, 2000)[b % 4] for b in range(B)]
+        logits = torch.full((B, V), low, dtype=DT[dt])
+        logits[:, -1] = top
+        light = np.array([(k - 1) * w for k in top_k])
+        border = light / (1 + light)  # where the peak begins
+        for off in (2 * TOL, -2 * TOL):
+            u = np.float32(border + off)
+            token = draw(logits, u, 1.0, top_k)
+            for b in range(B):
+                if float(u[b]) >= border[b] + TOL:
+                    assert token[b] == V - 1, (top_k[b], token[b])
+                elif 0 < float(u[b]) <= border[b] - TOL:  # the token whose interval holds u, or one within TOL
+                    total = 1 + light[b]
+                    assert abs(float(u[b]) * total - token[b] * w) <= TOL + w and token[b] < top_k[b] - 1, (top_k[b], token[b])
