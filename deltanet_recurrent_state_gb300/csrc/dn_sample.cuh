@@ -26,9 +26,9 @@
 // summed on fixed grids, 2^-43 of the largest over a row, where the order of a sum does not matter. 32-bit arithmetic would give another
 // token than 64 bits do for one random number in some thousands over a flat row; this does for one in 10^7.
 // That costs some 59 issue slots a token, and 32-bit arithmetic 13. So tokens of less than 2^-14 of the largest weight are summed in
-// 32 bits at first. Where they make up less than 2^-10 of the row, their errors, of either sign and some 2^-21 each over
-// thousands of tokens, leave the sums right to 2^-36 as well; else (and near the maximum always) the result
-// counts only if no border lies within their error's bound, and the row is summed again exactly if one does.
+// 32 bits at first, and the result counts only if no border lies within their error's bound (errors of equal tokens, and that of the
+// scale, have one sign, so their averaging out is not counted on). The row is summed again exactly if one does: where light tokens make up a share f of
+// a row, that is a row in 1 / f or fewer. With a top_p all tokens are taken exactly at once where that share is above 2^-10.
 //
 // What bounds it: a call of few rows is a chain of dependent steps (loads, four block and three cluster barriers, the comparison);
 // one of many rows the arithmetic of those that need the mass of the whole row, with HBM's share at 11.5 us for 256 rows of 151,936 in
@@ -69,8 +69,8 @@ constexpr int kSome = 512;           // listed tokens that are put together besi
 constexpr int kFew = 256;            // listed tokens that are compared each with each
 constexpr float kTail = 14.f;        // the negative binary logarithm of a weight that is summed in 32 bits at first
 constexpr int kTailShift = 10;       // all of those make up much of a row from 2^-10 of it on
-constexpr int kTailError = 16;       // and their sum is off by less than 2^-16: y by 2^-22.7 of itself (at 44, beyond which weights are below
-                                     // the grid, 2^-17.7 of the weight), the exponential by 2^-22, a sum of 32 by 2^-19
+constexpr int kTailError = 16;       // their sum is off by less than 2^-16: y by 2^-22.3 of itself (at 60, where 400,000 such weights make up 2^-41, 2^-16.9
+                                     // of the weight), the exponential by 2^-22, a sum of 32 by 2^-19
 constexpr int kFixed = 43;           // sums over a row are in units of 2^-43 of the largest weight: 2^19 of them fit 64 bits
 constexpr int kList = 50;            // over listed tokens, and a warp's tokens: units of 2^-50, 12,500 tokens
 constexpr int kFine = 56;            // a token's own weight, and what a warp adds up below the units of a row: 2^-56
@@ -257,11 +257,21 @@ __device__ __forceinline__ u64 rest_of(long long fine) { return (u64)((fine + (1
 __device__ __forceinline__ u64 mass_of(unsigned n, u64 weight) {
     return (__umul64hi(n, weight) << (64 - kFine + kFixed)) | (n * weight >> (kFine - kFixed));
 }
-__device__ __forceinline__ unsigned fewest_of(u64 need, u64 weight) {
-    unsigned n = (unsigned)((double)need * (double)(1 << (kFine - kFixed)) / (double)weight);  // off by one at most
+static __device__ __noinline__ unsigned fewest_of(u64 need, u64 weight) {
+    unsigned n = (unsigned)(__ull2float_rn(need) * (float)(1 << (kFine - kFixed)) / __ull2float_rn(weight));  // 2^19 at most, so off by one at most
     while (mass_of(n, weight) < need) ++n;
     while (n > 0 && mass_of(n - 1, weight) >= need) --n;
     return n;
+}
+
+// Whether a value's tokens, with the mass before them and that up to them, begin before the goal or not, and reach it or not, and after
+// how many, whichever way the masses and the goal are off by less than `error` of one another.
+static __device__ __noinline__ bool certain(u64 before, u64 upto, u64 goal, u64 error, u64 weight) {
+    auto apart = [&](u64 mass) { return mass >= goal + error || goal >= mass + error; };
+    if (!apart(before) || !apart(upto)) return false;
+    if (before >= goal || upto < goal) return true;
+    const u64 need = goal - before;
+    return need > error && fewest_of(need - error, weight) == fewest_of(need + error, weight);
 }
 
 static __device__ __noinline__ u64 weight_called(float x, Scale c, const float2 *powers) { return weight_of(x, c, powers); }
@@ -688,8 +698,9 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
         }
         if ((m.n += VEC) == 64) {
             flush_mass(both, m);
-            m.exact = m.exact_above = Sum();
-            m.small = m.small_above = two(0.f);
+            m.exact = Sum();
+            m.small = two(0.f);
+            if (BOTH) m.exact_above = Sum(), m.small_above = two(0.f);
             m.n = 0;
         }
     };
@@ -1106,7 +1117,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
     }
 
     // ---- the exact masses, and what top_p keeps ----
-    bool heavy;  // the light tokens, in 32 bits, make up much of the row
+    u64 error;  // twice that of the light tokens' 32-bit sums: of a running mass and of its share of the whole
     u64 kept, kept_before, all_kept, tau_weight, tail;  // this warp's, of the warps before it, of the row; of a token at tau (2^-kFine)
     unsigned alike, alike_before, r;
     auto above_tau = [&](float x) { return x > tau; };
@@ -1136,6 +1147,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
                 if (w == warp) kept_before = cta_kept, alike_before = cta_alike;
                 cta_kept += s.scan64[w], cta_alike += s.scan32[w], cta_all += s.scan64b[w], cta_tail += s.scan64c[w];
             }
+            if (threadIdx.x == 0) s.done = 0;  // (until the CTA that has the token says otherwise, after the exchange)
             if ((int)threadIdx.x < ranks) {
                 *cluster.map_shared_rank(&s.kept[parity][rank], threadIdx.x) = cta_kept;
                 *cluster.map_shared_rank(&s.all[parity][rank], threadIdx.x) = cta_all;
@@ -1152,8 +1164,8 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
                 all_kept += s.kept[parity][i], all += s.all[parity][i], tail += s.tail[parity][i], all_alike += s.eq[parity][i];
             }
             parity ^= 1;
-            heavy = tail > all >> kTailShift;
-            if (heavy && p < 1.f) {
+            error = tail >> (kTailError - 1);
+            if (tail > all >> kTailShift && p < 1.f) {
                 all_exact = true;
                 --tries;
                 continue;
@@ -1162,8 +1174,13 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
             r = tau > tau1 ? all_alike : r1;  // tokens at tau that may be kept
             if (!(p < 1.f)) break;
             if (r1) all += mass_of(r1, weight_at<kShort>(tau1, scale, s.powers));
-            const u64 goal = nucleus(all);
-            const bool more = all_kept >= goal, fewer = all_kept + mass_of(r, tau_weight) < goal;  // tau is higher, or lower
+            const u64 goal = nucleus(all), with_all = all_kept + mass_of(r, tau_weight);
+            const bool more = all_kept >= goal, fewer = with_all < goal;  // tau is higher, or lower
+            if (error && !certain(all_kept, with_all, goal, error, tau_weight)) {
+                all_exact = true;
+                --tries;
+                continue;
+            }
             if (!more && !fewer) {
                 r = fewest_of(goal - all_kept, tau_weight);
                 break;
@@ -1195,7 +1212,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
             tau = fmaxf(value_of<E>(now), tau1);
         }
 
-        // ---- the token: the first at which the kept mass passes u times the total ----
+        // ---- the token: the first at which the kept mass passes u times the total. Light tokens' errors may move that beyond a border ----
         const u64 all = all_kept + mass_of(r, tau_weight), goal = draw(all);
         auto mass = [&](u64 m, unsigned alike_upto) { return m + mass_of(min(alike_upto, r), tau_weight); };
         // the warp that has it; then its steps, which all warps share
@@ -1210,6 +1227,7 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
         const int chosen = s.chosen;
         int token = -1;
         float token_x = top;
+        bool sure = false;
         if (chosen >= 0) {
             int begin = chosen * per_warp, end = min(begin + per_warp, held);
             u64 kept_upto = s.scan64[0];
@@ -1246,7 +1264,6 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
             float mine_x = top;
             bool clear_of = false;
             u64 listed_upto = 0;  // of the tokens so far, in units of 2^-kList
-            const u64 error = heavy ? tail >> (kTailError - 1) : 0;  // of the running mass and of the total
             for (int v = begin; v < end; v += kThreads / VEC) {
                 const int i = v + (int)threadIdx.x / VEC;
                 float x = -kInf;
@@ -1291,22 +1308,23 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
             const unsigned who = __ballot_sync(0xffffffffu, mine >= 0 && mine == (place & (kFound - 1)));
             if (who) {
                 const int owner = __ffs(who) - 1;
-                const bool sure = !heavy || (place >= kFound && __shfl_sync(0xffffffffu, (int)clear_of, owner));
+                sure = place >= kFound && __shfl_sync(0xffffffffu, (int)clear_of, owner);
                 token_x = __shfl_sync(0xffffffffu, mine_x, owner);
                 token = base * VEC - head + (place & (kFound - 1));
-                if (heavy && lane < ranks) *cluster.map_shared_rank(&s.done, lane) = sure;  // all have to know
+                if (error && lane < ranks) *cluster.map_shared_rank(&s.done, lane) = sure;
             }
         }
-        if (heavy) {
-            cluster.sync();
-            if (!s.done) {
-                all_exact = true;
-                if (MODE == kEasy) {
-                    leave();
-                    return;
-                }
-                continue;
+        if (error) {  // all have to know whether the row is summed again
+            auto told = cluster.barrier_arrive();
+            if (token >= 0 && sure) finish(token, lane == 0 ? log_share(token_x, all, kFixed) : 0.f);
+            cluster.barrier_wait(std::move(told));
+            if (s.done) return;
+            all_exact = true;
+            if (MODE == kEasy) {
+                leave();
+                return;
             }
+            continue;
         }
         if (token >= 0) finish(token, lane == 0 ? log_share(token_x, all, kFixed) : 0.f);
         return;

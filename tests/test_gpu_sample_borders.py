@@ -172,3 +172,66 @@ def test_ties_far_below_the_largest(cuda, far, dt):
                 elif 0 < float(u[b]) <= border[b] - TOL:  # the token whose interval holds u, or one within TOL
                     total = 1 + light[b]
                     assert abs(float(u[b]) * total - token[b] * w) <= TOL + w and token[b] < top_k[b] - 1, (top_k[b], token[b])
+
+
+# ---- light tokens: a peak, and many tokens of less than 2^-14 of its weight ----
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("temperature", [1.0, 1.1, 1.3, 0.7])
+def test_a_share_of_light_tokens_below_the_limit(cuda, temperature, dt):
+    """Equal tokens that make up nearly 2^-10 of the row: their 32-bit sums have errors of one sign."""
+    V, top = 151936, 4.0
+    n = 150000
+    low = value(top + temperature * np.log(0.9 * 2.0 ** -10 / n), dt)
+    n = min(n, int(0.95 * 2.0 ** -10 / weight(low, top, temperature)))
+    check_equal_light(cuda, dt, V, top, low, temperature, n, n, 160)
+
+
+@pytest.mark.parametrize("dt", list(DT))
+def test_unequal_light_tokens_below_the_limit(cuda, dt):
+    """The same with a normal distribution of them, and a peak at the end."""
+    V = 151936
+    x = (2 * torch.randn(V, generator=torch.Generator().manual_seed(3), dtype=torch.float64)).to(DT[dt])
+    for temperature in (1.1, 1.3, 0.9):
+        rest = x[:-1].double().numpy()
+        t64 = float(np.float32(temperature))
+        x[-1] = float(t64 * np.log(np.exp(rest / t64).sum() / (0.9 * 2.0 ** -10)))
+        w = np.exp((x.double().numpy() - float(x[-1])) / t64)
+        part = w[:151900].reshape(-1, 100)  # (sums of 100, so that 64 bits are enough)
+        upto = np.concatenate([[0], np.cumsum(part.sum(1))[:-1]])[:, None] + np.cumsum(part, 1)
+        borders = upto.ravel() / (part.sum() + w[151900:].sum())
+        u = beside_borders(borders[50000:], 160)
+        want = np.searchsorted(borders, u, side="right")
+        token = draw(x[None].expand(len(u), V).contiguous(), u, temperature)
+        assert len(u) >= 100 and (token == want).all(), (temperature, (token != want).sum())
+
+
+@pytest.mark.parametrize("dt", list(DT))
+def test_top_p_among_light_tokens(cuda, dt):
+    """A share of light tokens below the limit, and a top_p whose border lies a few 10^-10 beside one of theirs."""
+    V, top, temperature = 40000, 4.0, 1.1
+    low = value(top + temperature * np.log(0.9 * 2.0 ** -10 / 39000), dt)
+    w = weight(low, top, temperature)
+    most = min(39000, int(0.98 * 2.0 ** -10 / w))
+    cases = []
+    for n in range(most - 6000, most):
+        for step in range(1, 400):
+            p = 1 - step * 2.0 ** -24
+            kept = (p * (1 + n * w) - 1) / w  # of the light tokens
+            off = (kept - np.rint(kept)) * w
+            if 1 < kept < n - 1 and 1.25 * TOL < abs(off) < 5e-10:
+                cases.append((n, p, int(np.ceil(kept))))
+    assert len(cases) >= 200
+    cases = cases[:: len(cases) // 160][:160]
+    logits = torch.full((len(cases), V), -float("inf"), dtype=DT[dt])
+    u = float(np.float32(1 - 2.0 ** -24))
+    for b, (n, _, _) in enumerate(cases):
+        logits[b, 0] = top
+        logits[b, 1:n + 1] = low
+    token = draw(logits, u, temperature, 0, [c[1] for c in cases])
+    for b, (n, p, kept) in enumerate(cases):
+        total = 1 + kept * w
+        # the last kept token, or one before it: total * 2^-24 from the end; a border that is as near as TOL leaves two
+        want = {int(np.floor((float(u) * total + s * TOL - 1) / w)) + 1 for s in (-1, 1)}
+        assert int(token[b]) in want, (n, p, kept, token[b], want)
