@@ -508,11 +508,13 @@ __device__ __forceinline__ void sample_row(const SampleArgs &a, Shared &s, uint4
         const float y = distance(x) * kCountScale;
         return y < (float)kBins ? (int)y : kBins;
     };
-    // the bin of a mass is given by its exponent and the upper four bits of its fraction, and its share by its upper 16 bits
+    // the bin of a mass is given by its exponent and the upper four bits of its fraction, and its share by its upper 16 bits; fewer for
+    // a CTA of more than 2^16 tokens, all of which may lie in one bin of 32 bits
+    const int dropped = max(0, 16 - __clz(per_cta * VEC - 1));
     auto mass_bits = [&](float x) { return (unsigned)__float_as_int(exp2_fast(scale.sharp ? (x == top ? 0.f : -200.f) : (x - top) * scale.ch)); };
     auto mass_bin = [&](unsigned bits) { return 0x7f0 - (int)(bits >> 19); };
-    auto mass_share = [&](unsigned bits) { return ((bits & 0x7fffffu) | 0x800000u) >> 8; };
-    auto mass_unit = [&](int bin) { return __int_as_float((0x3f800000 - (bin << 19)) & 0x7f800000); };  // of 2^-15, in the weight's octave
+    auto mass_share = [&](unsigned bits) { return ((bits & 0x7fffffu) | 0x800000u) >> (8 + dropped); };
+    auto mass_unit = [&](int bin) { return __int_as_float(((0x3f800000 - (bin << 19)) & 0x7f800000) + (dropped << 23)); };  // of 2^-15, in the weight's octave
     // this thread's vectors f(u), and its tokens f(x)
     auto each_vector = [&](auto f) {
         if (HELD) {

@@ -235,3 +235,44 @@ def test_top_p_among_light_tokens(cuda, dt):
         # the last kept token, or one before it: total * 2^-24 from the end; a border that is as near as TOL leaves two
         want = {int(np.floor((float(u) * total + s * TOL - 1) / w)) + 1 for s in (-1, 1)}
         assert int(token[b]) in want, (n, p, kept, token[b], want)
+
+
+# ---- histograms of masses: more tokens of a CTA in one bin than 32 bits hold as 16-bit shares ----
+
+
+@pytest.mark.parametrize("B,V", [(40, 151936), (60, 151936), (20, 400000)])
+def test_nearly_constant_rows_of_a_few_ctas(cuda, B, V):
+    """Right, and in few passes: a row costs no more than six times one of the same values that has eight CTAs."""
+    g = torch.Generator().manual_seed(B)
+    logits = torch.randn((B, V), generator=g)
+    u = torch.rand(B, generator=g).numpy()
+    token = draw(logits, u, 1000.0, 0, 0.95)
+    for b in range(0, B, 9):
+        x = logits[b].double().numpy()
+        w = np.exp((x - x.max()) / 1000.0)
+        order = np.argsort(-x, kind="stable")
+        upto = np.cumsum(w[order])
+        kept = np.sort(order[: int(np.searchsorted(upto, float(np.float32(0.95)) * upto[-1])) + 1])
+        upto = np.cumsum(w[kept]) / w[kept].sum()
+        i = int(np.searchsorted(kept, token[b]))
+        assert i < len(kept) and kept[i] == token[b]
+        # (64-bit sums of 150,000 are right to 10^-11)
+        assert (upto[i - 1] if i else 0.0) - TOL - 1e-11 <= u[b] <= upto[i] + TOL + 1e-11
+
+    def timed(rows):
+        args = [logits[:rows, None].cuda(), torch.zeros((rows, 1), dtype=torch.int32, device="cuda"), torch.tensor(u[:rows, None]).cuda(),
+                torch.full((rows,), 1000.0, device="cuda"), None, torch.full((rows,), 0.95, device="cuda")]
+        ws = dn.sample_workspace(rows, 1, V, cuda)
+        times = []
+        for _ in range(6):
+            start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            start.record()
+            for _ in range(5):
+                dn.dn_accept_sampled(*args, workspace=ws)
+            end.record()
+            torch.cuda.synchronize()
+            times.append(start.elapsed_time(end))
+        return min(times)
+
+    few = timed(9)  # eight CTAs a row, below the limit
+    assert timed(B) < 6 * (8 / (4 if V == 400000 else 2)) * few
