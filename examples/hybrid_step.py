@@ -71,7 +71,7 @@ class HybridModel:
         start = torch.tensor([0, n], dtype=torch.int32, device=self.device)
         x = self.embed[tokens]
         h, _ = dn.dn_residual_norm(None, x, eps=EPS)
-        for d in self.layers:
+        for i, d in enumerate(self.layers):
             if d["kind"] == "recurrent":
                 q, k, v = (h @ d["qkv"]).view(1, n, 3 * HEADS, DIM).split(HEADS, dim=2)
                 q, k = (torch.nn.functional.normalize(z.float(), dim=-1).half() for z in (q, k))
@@ -94,7 +94,11 @@ class HybridModel:
                 order, act = "gate", "sigmoid"
             if "gate" in d:
                 o = dn.dn_head_norm(o, (h @ d["gate"]).view(o.shape), order=order, act=act)
-            h, _ = dn.dn_residual_norm(o.reshape(n, -1) @ d["out"], x, eps=EPS)  # x is added to in place
+            y = o.reshape(n, -1) @ d["out"]
+            if i + 1 < len(self.layers):
+                h, _ = dn.dn_residual_norm(y, x, eps=EPS)  # x is added to in place, and the next layer reads its norm
+            else:
+                x += y  # (this model's head reads the stream itself)
         return x @ self.head
 
     def prompt(self, tokens):
