@@ -553,6 +553,8 @@ def rope_freqs(rot, base=10000.0, scaling=None, factor=1.0, context=4096, device
     than the `context` tokens a model was trained on: "linear" divides every frequency by factor; "base" raises the base so that
     the slowest pair is slowed by factor and the fastest stays; "ramp" keeps pairs that turn 32 times or more in
     `context` tokens, divides those that turn once or less, goes linearly between, and grows the amplitude by 0.1 ln(factor).
+    The line is one in a pair's turns, f * (w + (1 - w) / factor) with w = (turns - 1) / 31. A model that was trained with other borders, or with a line in
+    the pair's number j, needs frequencies of its own: round(turns a token * 2^64) as int64.
     """
     _require(rot >= 2 and rot % 2 == 0 and base > 1.0 and factor >= 1.0 and context > 0, "rot even, base > 1, factor >= 1, context > 0")
     _require(scaling in (None, "linear", "base", "ramp"), 'scaling None, "linear", "base" or "ramp"')

@@ -130,6 +130,17 @@ def turns_of(freqs):
     return [int(f) / 2.0 ** 64 for f in freqs]
 
 
+def test_rope_freqs_on_the_ramp():
+    """Pairs that turn 8.75, 16.5 and 24.25 times in the context are a quarter, a half and three quarters of the way, and those of 1 and 32 turns its ends."""
+    for factor, context in ((4.0, 4096), (2.0, 1000)):
+        for turns, way in ((8.75, 0.25), (16.5, 0.5), (24.25, 0.75), (1.0, 0.0), (32.0, 1.0), (0.5, 0.0), (40.0, 1.0)):
+            base = (context / (2 * math.pi * turns)) ** 2  # pair 16 of 32 turns base^(-1/2) radians a token
+            plain, _ = binding.rope_freqs(64, base=base, device="cpu")
+            ramp, _ = binding.rope_freqs(64, base=base, scaling="ramp", factor=factor, context=context, device="cpu")
+            assert abs(turns_of(plain)[16] * context - turns) < 1e-9
+            assert abs(turns_of(ramp)[16] * context - turns * (way + (1 - way) / factor)) < 1e-9
+
+
 def test_rope_freqs():
     freqs, amplitude = binding.rope_freqs(64, base=1e6, device="cpu")
     assert amplitude == 1.0 and freqs.dtype == torch.int64 and freqs.shape == (32,)
