@@ -220,7 +220,8 @@ template <typename T> void launch_head(const HeadArgs &a) {
                    a.order, a.act, static_cast<const T *>(a.x), a.x_stride, static_cast<const T *>(a.gate), a.gate_stride,
                    static_cast<const T *>(a.weight), a.inv_d, a.eps, static_cast<T *>(a.out));
     };
-    // one piece a warp against four (16 bits): 680 rows of 48 heads of 128 (2^19 groups) 5.6 against 5.8 us, 2,000 rows 13.9 against 11.9
+    // one piece a warp against four (16 bits): 680 rows of 48 heads of 128 (2^19 groups) 5.4 against 5.6 us, 1,020 rows 7.4 against 7.0, 2,000 rows 13.6
+    // against 11.8; against two (fp32): 170 rows 2.95 against 3.00, 680 rows 6.3 and 6.3, 1,020 rows 8.8 against 8.5, 2,000 rows 22.0 against 21.6
     if (a.groups <= 1u << 19) go(std::integral_constant<int, 1>{});
     else go(std::integral_constant<int, sizeof(T) == 4 ? 2 : 4>{});
 }

@@ -8,7 +8,8 @@
 // Angles. A frequency is given as turns a token in 64-bit fractions of a turn, so position * frequency in 64-bit integers drops
 // the whole turns exactly, however far the position; the upper 32 bits, as a signed fraction of a turn, are the angle
 // to 2^-32 of a turn. Its sine and cosine come from the special function unit: in -pi .. pi its absolute error is
-// below 2^-21, an eighth of a unit in the last place of the 16-bit (let alone 8-bit) results of the largest elements.
+// below 2^-21. With the products a turned element is off by less than 2^-19.5 of its pair's size, 1/360 of the unit in the last place
+// that fp16 has for the larger of the two. (One 8-bit element in 10^5 is rounded to another value than from an angle of 64 bits.)
 // A lane holds the same columns of every head of its token, so a warp computes them once for all its passes.
 //
 // What bounds it: memory at a prompt (every element read once and written once), latency at a verify block, where a
@@ -214,8 +215,11 @@ template <int D, bool BF, bool KV8, bool PAIRS> void launch_rope(RopeArgs a, cud
         const unsigned blocks = (unsigned)(((long long)a.pool.total * a.pieces + kWarps - 1) / kWarps);
         launch_pdl(rope_append_kernel<D, BF, KV8, PAIRS, P>, dim3(blocks), dim3(32 * kWarps), 0, st, a);
     };
-    // few rows: one pass a warp, so that they run at once (16 tokens 2.8 us); many: four (three 95, two 101, six 91 us for 25,000 tokens)
-    if ((long long)a.pool.total * passes <= 152 * 32) {
+    // few rows: one pass a warp, so that they run at once (16 tokens 2.8 us); many: four (three 95, two 101, six 91 us for 25,000 tokens).
+    // One against four at 1,200, 2,400, 4,900 and 9,700 warps of one pass: 48 heads of 128 into 8 bits 2.9, 3.2, 3.9, 6.5 against 3.5, 3.6, 4.1, 5.4 us;
+    // into 16 bits 2.6, 3.1, 3.7, 6.2 against 3.0, 3.1, 3.5, 4.8; 24 heads of 64 2.6, 2.9, 3.5, 5.9 against 2.8, 3.0, 3.9, 5.5;
+    // 32 heads of 256 3.0, 3.4, 4.8, 7.9 against 3.2, 3.2, 3.7, 4.9
+    if ((long long)a.pool.total * passes <= 32ll * device_sm_count()) {
         go(std::integral_constant<int, 1>{});
     } else {
         go(std::integral_constant<int, kPasses>{});
