@@ -521,7 +521,8 @@ unsigned int dn_attn_wait_timeouts(void);
  *   kept: the first top_k; of these those with w_i >= min_p; of these the shortest prefix with at least top_p of their mass
  *   target = the least i with  sum of kept w_j, j <= i  >  u * sum of all kept w_j;  logprob = log(w_target / that sum)
  * temperature <= 0 (or NaN), or top_p <= 0, keeps the first token alone (dn_accept_greedy's). top_k < 1 or >= V, top_p >= 1 (or NaN)
- * and min_p <= 0 (or NaN) keep all; min_p > 1 counts as 1. u below 0 (or NaN) counts as 0, and u >= 1 gives the last kept token.
+ * and min_p <= 0 (or NaN) keep all; min_p > 1 counts as 1. u below 0 (or NaN) counts as 0, and u >= 1 gives the last kept token, or
+ * one before it if those behind that one have less than 2^-41 of the largest weight in all.
  * Other temperatures count as the nearest one of 10^-30 .. 10^36 (infinity as 10^36).
  *
  *   logits        [B][T][V] DN_F16, DN_BF16 or DN_F32, 16-byte aligned; -inf marks a masked entry (never drawn) and NaN counts as

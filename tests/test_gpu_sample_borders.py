@@ -276,3 +276,27 @@ def test_nearly_constant_rows_of_a_few_ctas(cuda, B, V):
 
     few = timed(9)  # eight CTAs a row, below the limit
     assert timed(B) < 6 * (8 / (4 if V == 400000 else 2)) * few
+
+
+# ---- the last kept token ----
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("B,V", [(4, 600), (4, 40000), (100, 40000)])
+def test_random_numbers_of_one_and_more(cuda, B, V, dt):
+    """They give the last kept token, and may leave out one of less than 2^-41 of the largest weight."""
+    top = 20.0
+    last = [40.5, 60.0, 42.5]  # a row's last token's weight, in octaves below the largest
+    logits = torch.full((B, V), value(top - 12.0, dt), dtype=DT[dt])
+    logits[:, 5] = top
+    for i in range(3):
+        logits[i::3, -1] = value(top - last[i] * np.log(2.0), dt)
+    light = np.arange(B) % 3 != 0
+    for u in (1.0, 2.0, float("inf")):
+        for top_k in (0, V):
+            token = draw(logits, u, 1.0, top_k)
+            assert ((token == V - 1) | (light & (token == V - 2))).all()
+    logits[:, 10:-1] = -float("inf")  # few tokens are left: they are listed, in finer units
+    for top_k in (V, 200):
+        token = draw(logits, 1.0, 1.0, top_k)
+        assert ((token == V - 1) | (light & (token == 9))).all()
