@@ -32,9 +32,12 @@
 //
 // What bounds it: a call of few rows is a chain of dependent steps (loads, four block and three cluster barriers, the comparison);
 // one of many rows the arithmetic of those that need the mass of the whole row, with HBM's share at 11.5 us for 256 rows of 151,936 in
-// 16 bits. Measured on a GB300, us: one row of 151,936 in fp16 with top_k 40 and top_p 0.9 10.7, with top_p 0.95 alone 12.9,
-// without filters 12.6, at temperature 4 with top_p 0.95 49; 16 rows 13.8, 17.0, 16.9, 69; 256 rows in bf16 26.6, 47.3, 52.8, 540, and 47 with a
-// mixture of the first three (85 if a row of it keeps thousands of tokens).
+// 16 bits. Measured on a GB300, us: one row of 151,936 in fp16 with top_k 40 and top_p 0.9 11.1, with top_p 0.95 alone 13.1,
+// without filters 13.4, at temperature 4 with top_p 0.95 51; 16 rows 13.9, 17.2, 18.1, 73; 256 rows in bf16 26.3, 47.3, 55.5, 580, and 48 with a
+// mixture of the first three (87 if a row of it keeps thousands of tokens, or has to be summed again exactly).
+// Registers: 64 a thread in every kernel, so that two CTAs fit an SM. Spilled, bytes of stores and loads: kEasy 12 to 44 and 12 to 76, kAll held 146 to 166 and
+// 140 to 160, not held 486 to 554 and 720 to 780, kHard held 278 to 350 and 638 to 722, not held 1,580 to 1,600 and 1,590 to 1,610.
+// (With 128 registers and one CTA an SM kHard, held, spills nothing: one flat row among 256 then takes 80 for 87, but 256 of them 773 for 580.)
 #pragma once
 
 #include <algorithm>
@@ -1407,7 +1410,7 @@ template <typename E, bool HELD, Mode MODE> dn_status launch_sample_as(const Sam
 // each, of more than a vector a thread, leave the hard ones to a second kernel.
 // Measured, us, rows of 151,936: top_k 40 with top_p 0.9 and 1, 2, 4, 8 CTAs a row: 16 rows 17.5, 15.3, 13.5, 13.2; 80 rows 17.3, 27.2, 24.0,
 // 33.5; 256 rows 25.1, 56.8, 58.3, 89.3. The second kernel costs 1.8 where no row is hard; 256 rows of which one keeps thousands of tokens take
-// 165 without it and 85 with it. Clusters of 16 in it: 83, but those need not fit every GPU.
+// 165 without it and 87 with it. Clusters of 16 in it: 83, but those need not fit every GPU.
 template <typename E> dn_status launch_sample(SampleArgs a, cudaStream_t st) {
     const int vecs = (a.V + 2 * kVecOf<E> - 2) / kVecOf<E>;  // wherever a row begins
     const long long rows = (long long)a.B * a.T;
