@@ -220,10 +220,9 @@ __device__ __forceinline__ Weights weights_of(float x0, float x1, const Scale &c
     const float2 zl = __ffma2_rn(__fmul2_rn(g, g), __ffma2_rn(g, __ffma2_rn(g, __ffma2_rn(g, two(0.00833333333f), two(0.0416666667f)), two(0.166666667f)), two(0.5f)), gl);
     const float2 b0 = powers[k0 & 15], b1 = powers[k1 & 15];
     const float2 bh = make_float2(b0.x, b1.x), bl = make_float2(b0.y, b1.y);
-    const float2 ph = __fmul2_rn(bh, gh);
-    const float2 pl = __fadd2_rn(__ffma2_rn(bh, gh, __fmul2_rn(bh, ngh)), __ffma2_rn(bl, gh, __fmul2_rn(bh, zl)));
-    const float2 hi = __fadd2_rn(bh, ph);
-    const float2 lo = __fadd2_rn(__fadd2_rn(__ffma2_rn(hi, two(-1.f), bh), ph), __fadd2_rn(bl, pl));
+    // (no product that is rounded by itself meets a sum: the compiler may make one operation of the two, and hi + lo would then count its rounding twice)
+    const float2 hi = __ffma2_rn(bh, gh, bh);
+    const float2 lo = __fadd2_rn(__ffma2_rn(bh, gh, __ffma2_rn(hi, two(-1.f), bh)), __fadd2_rn(bl, __ffma2_rn(bl, gh, __fmul2_rn(bh, zl))));
     const float2 power = make_float2(__int_as_float((127 + (k0 >> 4)) << 23), __int_as_float((127 + (k1 >> 4)) << 23));
     return Weights{__fmul2_rn(hi, power), __fmul2_rn(lo, power)};
 }

@@ -278,6 +278,37 @@ def test_nearly_constant_rows_of_a_few_ctas(cuda, B, V):
     assert timed(B) < 6 * (8 / (4 if V == 400000 else 2)) * few
 
 
+# ---- one weight at a time ----
+
+
+@pytest.mark.parametrize("dt", list(DT))
+@pytest.mark.parametrize("V", [1800, 20000])
+def test_weights_of_many_sizes(cuda, V, dt):
+    """Equal tokens before a peak, other ones in every row, a few octaves below it: their one weight decides where the peak begins, and a random number lies
+    beside that place."""
+    rng = np.random.default_rng(V)
+    N = 400000
+    temperature = np.exp(rng.uniform(-1, 1, N)).astype(np.float32)
+    low = torch.tensor(3.0 - temperature * rng.uniform(0.05, 7.0, N)).to(DT[dt]).double().numpy()
+    w = np.exp((low - 3.0) / temperature.astype(np.float64))
+    n = np.clip(np.rint(rng.uniform(0.4, 0.9, N) / w), 1, 1700).astype(np.int64)
+    border = n * w / (1 + n * w)
+    u = border.astype(np.float32)
+    off = u - border
+    chosen = np.flatnonzero((np.abs(off) > 1.25 * TOL) & (np.abs(off) < 1.6e-10))[:400]
+    assert len(chosen) >= 300
+    logits = torch.full((len(chosen), V), -float("inf"), dtype=DT[dt])
+    for b, i in enumerate(chosen):
+        logits[b, : n[i]] = float(low[i])
+        logits[b, n[i]] = 3.0
+    want = np.where(off[chosen] < 0, n[chosen] - 1, n[chosen])
+    for top_k in (0, V, 1701):
+        token = draw(logits, u[chosen], temperature[chosen], top_k)
+        assert (token == want).all(), (token != want).sum()
+    for b in range(0, len(chosen), 20):  # a row alone
+        assert draw(logits[b:b + 1], u[chosen[b]], temperature[chosen[b]])[0] == want[b]
+
+
 # ---- the last kept token ----
 
 
