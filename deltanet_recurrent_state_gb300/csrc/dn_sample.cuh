@@ -25,18 +25,18 @@
 // series; P. T. P. Tang, "Table-driven implementation of the exponential function in IEEE floating-point arithmetic", 1989), and
 // summed on fixed grids, 2^-43 of the largest over a row, where the order of a sum does not matter. 32-bit arithmetic would give another
 // token than 64 bits do for one random number in some thousands over a flat row; this does for one in 10^7.
-// That costs some 59 issue slots a token, and 32-bit arithmetic 13. So tokens of less than 2^-14 of the largest weight are summed in
+// That costs some 57 issue slots a token, and 32-bit arithmetic 13. So tokens of less than 2^-14 of the largest weight are summed in
 // 32 bits at first, and the result counts only if no border lies within their error's bound (errors of equal tokens, and that of the
 // scale, have one sign, so their averaging out is not counted on). The row is summed again exactly if one does: where light tokens make up a share f of
 // a row, that is a row in 1 / f or fewer. With a top_p all tokens are taken exactly at once where that share is above 2^-10.
 //
 // What bounds it: a call of few rows is a chain of dependent steps (loads, four block and three cluster barriers, the comparison);
 // one of many rows the arithmetic of those that need the mass of the whole row, with HBM's share at 11.5 us for 256 rows of 151,936 in
-// 16 bits. Measured on a GB300, us: one row of 151,936 in fp16 with top_k 40 and top_p 0.9 11.1, with top_p 0.95 alone 13.1,
-// without filters 13.4, at temperature 4 with top_p 0.95 51; 16 rows 13.9, 17.2, 18.1, 73; 256 rows in bf16 26.3, 47.3, 55.5, 580, and 48 with a
-// mixture of the first three (87 if a row of it keeps thousands of tokens, or has to be summed again exactly).
-// Registers: 64 a thread in every kernel, so that two CTAs fit an SM. Spilled, bytes of stores and loads: kEasy 12 to 44 and 12 to 76, kAll held 146 to 166 and
-// 140 to 160, not held 486 to 554 and 720 to 780, kHard held 278 to 350 and 638 to 722, not held 1,580 to 1,600 and 1,590 to 1,610.
+// 16 bits. Measured on a GB300, us: one row of 151,936 in fp16 with top_k 40 and top_p 0.9 11.3, with top_p 0.95 alone 13.4,
+// without filters 13.6, at temperature 4 with top_p 0.95 50; 16 rows 14.1, 17.4, 18.2, 71; 256 rows in bf16 26.4, 47.5, 55.3, 568, and 48 with a
+// mixture of the first three (88 if a row of it keeps thousands of tokens, or has to be summed again exactly).
+// Registers: 64 a thread in every kernel, so that two CTAs fit an SM. Spilled, bytes of stores and loads: kEasy 16 to 48 and 24 to 80, kAll held 190 and
+// 200, not held 510 to 570 and 740 to 800, kHard held 320 to 360 and 690 to 800, not held 1,600 to 1,650 and 1,460 to 1,630.
 // (With 128 registers and one CTA an SM kHard, held, spills nothing: one flat row among 256 then takes 80 for 87, but 256 of them 773 for 580.)
 #pragma once
 
@@ -1409,7 +1409,7 @@ template <typename E, bool HELD, Mode MODE> dn_status launch_sample_as(const Sam
 // each, of more than a vector a thread, leave the hard ones to a second kernel.
 // Measured, us, rows of 151,936: top_k 40 with top_p 0.9 and 1, 2, 4, 8 CTAs a row: 16 rows 17.5, 15.3, 13.5, 13.2; 80 rows 17.3, 27.2, 24.0,
 // 33.5; 256 rows 25.1, 56.8, 58.3, 89.3. The second kernel costs 1.8 where no row is hard; 256 rows of which one keeps thousands of tokens take
-// 165 without it and 87 with it. Clusters of 16 in it: 83, but those need not fit every GPU.
+// 165 without it and 88 with it. Clusters of 16 in it: 83, but those need not fit every GPU.
 template <typename E> dn_status launch_sample(SampleArgs a, cudaStream_t st) {
     const int vecs = (a.V + 2 * kVecOf<E> - 2) / kVecOf<E>;  // wherever a row begins
     const long long rows = (long long)a.B * a.T;
